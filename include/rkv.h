@@ -12,6 +12,10 @@
  *   [IndexMem]  "IndexMem: learned KV eviction with latent memory" (only
  *               its latent memory for evicted tokens)
  *
+ * and of four operators around the step: attention over whole prompts, many
+ * tokens at a time into the cache, attention of drafted tokens, and copying,
+ * moving and freeing whole sequences.
+ *
  * Conventions shared by every entry point
  * ---------------------------------------
  * - Every call returns an int status: RKV_OK (0) or a negative RKV_ERR_*.
@@ -434,6 +438,119 @@ RKV_API int rkv_decode_step(const rkv_cache_t *cache, const int32_t *t, const in
                             const float *q, float scale, const void *k_new, const void *v_new,
                             const float *lb_new, const rkv_select_t *sel, float *out, float *lse_kept,
                             float *dropped, void *ws, size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * The operators around the decode step: the prompt before the first
+ * eviction, many tokens at a time into the cache, drafted tokens, and whole
+ * sequences.  They have no counterpart in the papers.
+ *
+ * Packed sequences: `cu` is a device array of B + 1 offsets; the tokens of
+ * sequence b are rows cu[b] .. cu[b+1] - 1 of the packed arrays (B <= 1024;
+ * sequences may be empty).  Offsets that are negative, decrease or pass the
+ * given number of rows are recorded as RKV_DEV_BAD_INPUT, and the call then
+ * does nothing.  Rows before cu[0] and from cu[B] on are neither read nor
+ * written. */
+
+/* ---------------------------------------------------------------------------
+ * rkv_prompt_attn -- causal grouped-query attention over the whole prompts
+ * of a batch, for one layer.  Token i of a sequence attends tokens 0 .. i of
+ * the same sequence:
+ *   out[i,hq] = sum_{j<=i} exp(z_ij - lse_i) v[j,hq/G],
+ *   z_ij = scale * <q[i,hq], k[j,hq/G]>,  lse_i = log sum_{j<=i} exp(z_ij)
+ * Only B, H, Hq, D and dtype of the cache are used; its pools are not read.
+ * Sums and softmax statistics are fp32; with RKV_BF16 the softmax weights are
+ * rounded to bf16 for the product with V and out once at the end.
+ *   q         [n_tokens][Hq][D] of dtype, q_stride elements between tokens
+ *   k, v      [n_tokens][H][D] of dtype, k_stride / v_stride between tokens
+ *             (a slice of one projection's output, or one layer of
+ *             [n_tokens][L][H][D], needs no copy)
+ *   out       [n_tokens][Hq][D] of dtype, out_stride between tokens; must
+ *             not overlap the inputs
+ *   lse       [n_tokens][Hq] float or NULL
+ * Pointers and token strides (in bytes) must be multiples of 16.  A value of
+ * v that is infinite or NaN reaches only the rows that attend it.
+ * Errors: RKV_ERR_INVALID_ARG, RKV_ERR_UNSUPPORTED (D not 64 or 128, B > 1024),
+ * RKV_ERR_WORKSPACE_TOO_SMALL, RKV_ERR_CUDA.  Device: RKV_DEV_BAD_INPUT. */
+RKV_API int rkv_prompt_attn(const rkv_cache_t *cache, const int32_t *cu, int32_t n_tokens, const void *q,
+                            int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                            float scale, void *out, int64_t out_stride, float *lse, void *ws, size_t ws_bytes,
+                            void *stream);
+
+/* ---------------------------------------------------------------------------
+ * rkv_append_tokens -- rkv_append for many tokens of each sequence: the
+ * tokens of a prompt, or the accepted path of a drafted tree.  Slots
+ * len[c] .. of every head c of sequence b receive the sequence's n_b =
+ * cu[b+1] - cu[b] tokens in order, at positions pos0[b], pos0[b] + 1, ...;
+ * len[c] += n_b.  New pages are popped from the top of the free stack, heads
+ * in ascending c, each head's pages in ascending table index.
+ *   cu        [B+1] int32, offsets into tok (or into the rows, without tok)
+ *   tok       [n_new] int32, the row of each token, or NULL: row i is token i
+ *   pos0      [B] int32
+ *   k_new, v_new [n_rows][L][H][D] of the pool dtype, lb_new [n_rows][L][H]
+ * Errors: RKV_ERR_INVALID_ARG, RKV_ERR_UNSUPPORTED (rows that are not 128, 256
+ * or 512 bytes, B > 1024), RKV_ERR_WORKSPACE_TOO_SMALL, RKV_ERR_CUDA.  Device:
+ * RKV_DEV_TABLE_OVERFLOW (the head takes nothing), RKV_DEV_POOL_EXHAUSTED (the
+ * first head that finds too few pages and the later ones that need one take
+ * nothing), RKV_DEV_BAD_INPUT (negative len or pos0, a position past int32: the
+ * head takes nothing; a row of tok outside [0, n_rows): the slot is left as
+ * it was).  Two launches. */
+RKV_API int rkv_append_tokens(const rkv_cache_t *cache, const int32_t *cu, const int32_t *tok, int32_t n_new,
+                              const int32_t *pos0, const void *k_new, const void *v_new, const float *lb_new,
+                              int32_t n_rows, void *ws, size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * rkv_tree_attn -- attention of drafted tokens over the cache.  Each sequence
+ * has a tree (or any set) of n_b = cu[b+1] - cu[b] <= max_nodes drafted
+ * tokens; token i attends every kept cache entry of its sequence's heads and
+ * the drafted tokens j with bit j of mask[cu[b] + i] set (normally its
+ * ancestors and itself; bits from n_b on are ignored).  One token with mask
+ * 1 is a decode step whose own key counts.  The cache is not changed: after
+ * the verification rkv_append_tokens takes the accepted rows.
+ *   n_tokens  rows of the packed arrays; max_nodes in [1, 64]
+ *   q         [n_tokens][L][Hq][D] of the pool dtype
+ *   k_draft, v_draft [n_tokens][L][H][D] of the pool dtype
+ *   mask      [n_tokens] uint64
+ *   sel       selection of this step (only keep_mask is read), or NULL: every
+ *             entry is kept
+ *   out       [n_tokens][L][Hq][D] of the pool dtype (0 where a token
+ *             attends nothing)
+ *   lse       [n_tokens][L][Hq] float or NULL (-inf where nothing)
+ *   ws_bytes  at least rkv_tree_workspace_size(cache, max_nodes)
+ * Rounding and infinities as for rkv_prompt_attn; rows past a head's length
+ * and evicted rows may hold anything.
+ * Errors: RKV_ERR_INVALID_ARG, RKV_ERR_UNSUPPORTED (D not 64 or 128, B > 1024,
+ * Hq/H > 64), RKV_ERR_WORKSPACE_TOO_SMALL, RKV_ERR_CUDA.  Device:
+ * RKV_DEV_BAD_INPUT (also for a page id outside the pool: its rows count as
+ * evicted). */
+RKV_API int rkv_tree_attn(const rkv_cache_t *cache, const int32_t *cu, int32_t n_tokens, int32_t max_nodes,
+                          const void *q, const void *k_draft, const void *v_draft, const uint64_t *mask, float scale,
+                          const rkv_select_t *sel, void *out, float *lse, void *ws, size_t ws_bytes, void *stream);
+
+/* Bytes of workspace that serve rkv_tree_attn with trees of up to max_nodes
+ * tokens, and every other call on this cache shape (host only; 0 if the shape
+ * or max_nodes is invalid).  rkv_workspace_init clears it as any other. */
+RKV_API size_t rkv_tree_workspace_size(const rkv_cache_t *cache, int32_t max_nodes);
+
+/* ---------------------------------------------------------------------------
+ * rkv_fork_sequences -- let every sequence slot continue another: parallel
+ * samples of one prompt, the reordering of beams, the end of a sequence.
+ * After the call slot b holds the entries that slot parent[b] held before
+ * it, or nothing if parent[b] is -1.  Per sequence s that some slot
+ * continues, its pages go to slot s if parent[s] == s, else to the lowest
+ * such slot (block tables change, no row moves); every other such slot
+ * receives a copy in new pages, because compaction moves rows inside a page
+ * and so no page can belong to two heads.  The pages of a sequence that no
+ * slot continues are pushed onto the free stack first (heads in ascending c,
+ * pages in ascending table index); the copies' pages are then popped (heads
+ * in ascending c, pages in ascending table index).  Rows past a head's length
+ * are not copied; table entries past a head's pages become -1.
+ *   parent    [B] int32
+ * Errors: RKV_ERR_INVALID_ARG, RKV_ERR_UNSUPPORTED (B > 64, rows that are not
+ * 128, 256 or 512 bytes), RKV_ERR_WORKSPACE_TOO_SMALL, RKV_ERR_CUDA.  Device:
+ * RKV_DEV_POOL_EXHAUSTED (too few pages for all copies) or RKV_DEV_BAD_INPUT (a
+ * parent outside [-1, B)): nothing is changed.  Two launches. */
+RKV_API int rkv_fork_sequences(const rkv_cache_t *cache, const int32_t *parent, void *ws, size_t ws_bytes,
+                               void *stream);
 
 #ifdef __cplusplus
 }

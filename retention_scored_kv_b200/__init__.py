@@ -9,7 +9,8 @@ Entry points (same names as the C ABI, without the ``rkv_`` prefix):
 ``score_select``, ``score_select_budget`` (as ``score_select_per_head`` and
 ``score_select_contour``), ``paged_decode_attn``, ``dropped_mass``, ``eviction_error``,
 ``memory_update``, ``memory_read``, ``compact_pages``,
-``append``, ``decode_step``, ``workspace_size``, ``workspace_init``,
+``append``, ``decode_step``, ``prompt_attn``, ``append_tokens``, ``tree_attn``,
+``fork_sequences``, ``workspace_size``, ``workspace_init``,
 ``device_status``, ``version``, ``last_error``.  ``Cache``/``Selection``/
 ``Workspace`` hold the tensors and build the C structs; ``step`` runs one
 decode step, either as the separate calls select -> attention (+ dropped
@@ -36,7 +37,8 @@ EXPORTS = ("rkv_version", "rkv_last_error", "rkv_workspace_size", "rkv_workspace
            "rkv_workspace_set_wait_limit",
            "rkv_score_select", "rkv_score_select_budget", "rkv_paged_decode_attn", "rkv_dropped_mass",
            "rkv_eviction_error", "rkv_memory_update", "rkv_memory_read", "rkv_compact_pages", "rkv_append",
-           "rkv_decode_step")
+           "rkv_decode_step", "rkv_prompt_attn", "rkv_append_tokens", "rkv_tree_attn", "rkv_tree_workspace_size",
+           "rkv_fork_sequences")
 BUDGET_PER_HEAD, BUDGET_CONTOUR = 0, 1
 
 
@@ -83,6 +85,7 @@ def load(path: str | None = None):
                            "`python -m retention_scored_kv_b200.build`")
     lib = ctypes.CDLL(path)
     P, I, SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+    I32, I64 = ctypes.c_int32, ctypes.c_int64
     CP, SP = ctypes.POINTER(CacheStruct), ctypes.POINTER(SelectStruct)
     sig = {
         "rkv_version": (ctypes.c_char_p, []),
@@ -101,6 +104,11 @@ def load(path: str | None = None):
         "rkv_compact_pages": (I, [CP, SP, P, SZ, P]),
         "rkv_append": (I, [CP, P, P, P, P, P, SZ, P]),
         "rkv_decode_step": (I, [CP, P, P, P, ctypes.c_float, P, P, P, SP, P, P, P, P, SZ, P]),
+        "rkv_prompt_attn": (I, [CP, P, I32, P, I64, P, I64, P, I64, ctypes.c_float, P, I64, P, P, SZ, P]),
+        "rkv_append_tokens": (I, [CP, P, P, I32, P, P, P, P, I32, P, SZ, P]),
+        "rkv_tree_attn": (I, [CP, P, I32, I32, P, P, P, P, ctypes.c_float, SP, P, P, P, SZ, P]),
+        "rkv_tree_workspace_size": (SZ, [CP, I32]),
+        "rkv_fork_sequences": (I, [CP, P, P, SZ, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -204,10 +212,11 @@ class Selection:
 
 
 class Workspace:
-    """Caller-owned scratch of librkv, sized by rkv_workspace_size."""
+    """Caller-owned scratch of librkv, sized by rkv_workspace_size (or, with
+    ``max_nodes``, by rkv_tree_workspace_size: tree_attn needs that)."""
 
-    def __init__(self, cache: Cache, stream: torch.cuda.Stream | None = None):
-        self.nbytes = workspace_size(cache)
+    def __init__(self, cache: Cache, stream: torch.cuda.Stream | None = None, max_nodes: int = 0):
+        self.nbytes = tree_workspace_size(cache, max_nodes) if max_nodes else workspace_size(cache)
         self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=cache.len.device)
         workspace_init(self, stream)
 
@@ -237,6 +246,14 @@ def last_error() -> str:
 def workspace_size(cache: Cache) -> int:
     st = cache.struct()
     n = load().rkv_workspace_size(ctypes.byref(st))
+    if n == 0:
+        raise RkvError(ERR_INVALID_ARG, last_error())
+    return n
+
+
+def tree_workspace_size(cache: Cache, max_nodes: int) -> int:
+    st = cache.struct()
+    n = load().rkv_tree_workspace_size(ctypes.byref(st), int(max_nodes))
     if n == 0:
         raise RkvError(ERR_INVALID_ARG, last_error())
     return n
@@ -364,6 +381,92 @@ def decode_step(cache: Cache, t: torch.Tensor, m_global: torch.Tensor | None, q:
     _check(load().rkv_decode_step(ctypes.byref(cs), _ptr(t), _ptr(m_global), _ptr(q), ctypes.c_float(scale),
                                   _ptr(k_new), _ptr(v_new), _ptr(lb_new), ss, _ptr(out), _ptr(lse), _ptr(dropped),
                                   ctypes.c_void_p(ws.ptr), ws.nbytes, _stream(stream)))
+
+
+def _tokens(name: str, x: torch.Tensor, shape: tuple, dtype: torch.dtype, device) -> int:
+    """Address of a packed tensor [tokens, *shape]: only the token stride is free."""
+    if x.dtype != dtype or x.device != device or tuple(x.shape[1:]) != shape:
+        raise ValueError(f"{name}: {dtype} [tokens, {', '.join(map(str, shape))}] on {device} expected, got {x.dtype} "
+                         f"{tuple(x.shape)} on {x.device}")
+    n = 1
+    for size, stride in zip(reversed(shape), reversed(x.stride()[1:])):
+        if size > 1 and stride != n:
+            raise ValueError(f"{name}: the values of one token must be contiguous")
+        n *= size
+    return x.data_ptr()
+
+
+def _packed(name: str, x: torch.Tensor, n: int, shape: tuple, dtype: torch.dtype, device) -> int:
+    """Address of a contiguous tensor [n, *shape]."""
+    if tuple(x.shape) != (n, *shape) or x.dtype != dtype or x.device != device or not x.is_contiguous():
+        raise ValueError(f"{name}: contiguous {dtype} {(n, *shape)} on {device} expected, got {x.dtype} "
+                         f"{tuple(x.shape)} on {x.device}")
+    return x.data_ptr()
+
+
+def prompt_attn(cache: Cache, cu: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: float,
+                out: torch.Tensor, lse: torch.Tensor | None, ws: Workspace, stream=None):
+    """Causal attention over packed prompts, one layer: q and out [tokens, Hq, D],
+    k and v [tokens, H, D] of the pool dtype (the token stride is free), cu
+    int32 [B + 1], lse float32 [tokens, Hq] or None."""
+    n, dev, dt = q.shape[0], cache.len.device, cache.k_pool.dtype
+    if not n == k.shape[0] == v.shape[0] == out.shape[0]:
+        raise ValueError("q, k, v and out must have the same number of tokens")
+    hq, h, i32 = (cache.Hq, cache.D), (cache.H, cache.D), torch.int32
+    cs = cache.struct()
+    _check(load().rkv_prompt_attn(
+        ctypes.byref(cs), _packed("cu", cu, cache.B + 1, (), i32, dev), n,
+        _tokens("q", q, hq, dt, dev), q.stride(0), _tokens("k", k, h, dt, dev), k.stride(0),
+        _tokens("v", v, h, dt, dev), v.stride(0), float(scale), _tokens("out", out, hq, dt, dev), out.stride(0),
+        None if lse is None else _packed("lse", lse, n, (cache.Hq,), torch.float32, dev), ws.ptr, ws.nbytes,
+        _stream(stream)))
+
+
+def append_tokens(cache: Cache, cu: torch.Tensor, pos0: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
+                  lb_new: torch.Tensor, ws: Workspace, tok: torch.Tensor | None = None, stream=None):
+    """Append the packed tokens of every sequence to all its heads: k_new and
+    v_new [rows, L, H, D], lb_new float32 [rows, L, H]; token i is row tok[i]
+    (int32), or row i without tok; positions count up from pos0[b]."""
+    n, dev, lh = k_new.shape[0], cache.len.device, (cache.L, cache.H)
+    n_new = n if tok is None else tok.shape[0]
+    cs = cache.struct()
+    _check(load().rkv_append_tokens(
+        ctypes.byref(cs), _packed("cu", cu, cache.B + 1, (), torch.int32, dev),
+        None if tok is None else _packed("tok", tok, n_new, (), torch.int32, dev), n_new,
+        _packed("pos0", pos0, cache.B, (), torch.int32, dev),
+        _packed("k_new", k_new, n, (*lh, cache.D), cache.k_pool.dtype, dev),
+        _packed("v_new", v_new, n, (*lh, cache.D), cache.k_pool.dtype, dev),
+        _packed("lb_new", lb_new, n, lh, torch.float32, dev), n, ws.ptr, ws.nbytes, _stream(stream)))
+
+
+def tree_attn(cache: Cache, cu: torch.Tensor, q: torch.Tensor, k_draft: torch.Tensor, v_draft: torch.Tensor,
+              mask: torch.Tensor, scale: float, sel: Selection | None, out: torch.Tensor, lse: torch.Tensor | None,
+              ws: Workspace, max_nodes: int, stream=None):
+    """Attention of drafted tokens over the cache and one another: q and out
+    [tokens, L, Hq, D], k_draft and v_draft [tokens, L, H, D] of the pool dtype,
+    mask int64 [tokens] (bit j: attends drafted token j of its sequence), at
+    most max_nodes tokens a sequence; ws made with at least that max_nodes."""
+    n, dev, dt, L = q.shape[0], cache.len.device, cache.k_pool.dtype, cache.L
+    cs = cache.struct()
+    _check(load().rkv_tree_attn(
+        ctypes.byref(cs), _packed("cu", cu, cache.B + 1, (), torch.int32, dev), n, int(max_nodes),
+        _packed("q", q, n, (L, cache.Hq, cache.D), dt, dev),
+        _packed("k_draft", k_draft, n, (L, cache.H, cache.D), dt, dev),
+        _packed("v_draft", v_draft, n, (L, cache.H, cache.D), dt, dev),
+        _packed("mask", mask, n, (), torch.int64, dev), float(scale),
+        ctypes.byref(sel.struct()) if sel is not None else None,
+        _packed("out", out, n, (L, cache.Hq, cache.D), dt, dev),
+        None if lse is None else _packed("lse", lse, n, (L, cache.Hq), torch.float32, dev), ws.ptr, ws.nbytes,
+        _stream(stream)))
+
+
+def fork_sequences(cache: Cache, parent: torch.Tensor, ws: Workspace, stream=None):
+    """Slot b continues sequence parent[b] (int32 [B]; -1: the slot ends):
+    pages move to one continuing slot, the others get copies."""
+    cs = cache.struct()
+    _check(load().rkv_fork_sequences(ctypes.byref(cs),
+                                     _packed("parent", parent, cache.B, (), torch.int32, cache.len.device), ws.ptr,
+                                     ws.nbytes, _stream(stream)))
 
 
 @dataclass

@@ -120,6 +120,9 @@ void layout_for(const rkv_cache_t &c, int sel_groups_x_waves, WsLayout *L) {
     L->bfloor = take((size_t)C * 4, 256);
     L->bskip = take((size_t)C, 256);
     L->bseq = take((size_t)c.B * 16, 256);
+    L->seq_plan = take(8, 256);
+    L->seq_base = take((size_t)C * 4, 256);
+    L->seq_pop = take((size_t)C * 4, 256);
     L->total = take(0, 256);
 }
 
@@ -170,6 +173,44 @@ int encode_pool_map(CUtensorMap *m, void *pool, int D, int n_pages) {
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(RKV_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
     return RKV_OK;
+}
+
+// Packed sequences: offsets cu[B+1] into n rows.
+int check_packed(const char *what, const rkv_cache_t *c, const int32_t *cu, int32_t n) {
+    if (!cu) return fail(RKV_ERR_INVALID_ARG, "%s: cu is NULL", what);
+    if (n < 1) return fail(RKV_ERR_INVALID_ARG, "%s: the number of tokens must be positive (got %d)", what, n);
+    if (c->B > SERVE_MAX_B) return fail(RKV_ERR_UNSUPPORTED, "%s: at most %d sequences", what, SERVE_MAX_B);
+    if ((int64_t)n * c->Hq >= (1ll << 31)) return fail(RKV_ERR_UNSUPPORTED, "%s: tokens * Hq must be < 2^31", what);
+    return RKV_OK;
+}
+
+// Rows of `heads` heads per token, `stride` elements between tokens.
+int check_rows(const char *what, const rkv_cache_t *c, const void *p, int64_t stride, int heads) {
+    const int eb = elt_bytes(c->dtype);
+    if (!aligned16(p) || stride * eb % 16 != 0)
+        return fail(RKV_ERR_INVALID_ARG, "%s: pointer and token stride must be 16-byte aligned", what);
+    if (stride < (int64_t)heads * c->D || stride > (1ll << 36))
+        return fail(RKV_ERR_INVALID_ARG, "%s: token stride %lld is below heads*D", what, (long long)stride);
+    return RKV_OK;
+}
+
+// Row sizes that the sequence operators move.
+int check_moved(const char *what, const rkv_cache_t *c) {
+    const int rb = c->D * elt_bytes(c->dtype);
+    if (rb != 128 && rb != 256 && rb != 512)
+        return fail(RKV_ERR_UNSUPPORTED, "%s: rows of %d bytes are not built (128, 256 or 512)", what, rb);
+    return RKV_OK;
+}
+
+// The tree operator's tickets and records follow the shared workspace.
+TreeLayout tree_offsets(const rkv_cache_t &c, int max_nodes, size_t *ticket, size_t *rec, size_t *total) {
+    WsLayout L;
+    ws_layout(c, &L);
+    const TreeLayout t = tree_layout(c.dtype, c.D, c.Hq / c.H, (int64_t)c.B * c.L * c.H, max_nodes);
+    *ticket = L.total;
+    *rec = (*ticket + t.tickets * 4 + 255) / 256 * 256;
+    *total = *rec + t.rec_floats * 4;
+    return t;
 }
 
 template <typename T>
@@ -763,6 +804,195 @@ RKV_API int rkv_append(const rkv_cache_t *cache, const int32_t *t, const void *k
     a.row_bytes = cache->D * elt_bytes(cache->dtype);
     cudaError_t e = launch_append(a, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "append kernel launch");
+    return RKV_OK;
+}
+
+RKV_API int rkv_prompt_attn(const rkv_cache_t *cache, const int32_t *cu, int32_t n_tokens, const void *q,
+                            int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                            float scale, void *out, int64_t out_stride, float *lse, void *ws, size_t ws_bytes,
+                            void *stream) {
+    const NvtxRange nvtx_range("rkv_prompt_attn");
+    int rc = check_cache(cache, false);
+    if (rc) return rc;
+    if ((rc = check_packed("rkv_prompt_attn", cache, cu, n_tokens))) return rc;
+    if (!q || !k || !v || !out) return fail(RKV_ERR_INVALID_ARG, "rkv_prompt_attn: q, k, v and out must be non-NULL");
+    if (cache->D != 64 && cache->D != 128)
+        return fail(RKV_ERR_UNSUPPORTED, "rkv_prompt_attn: D = %d is not built (64 or 128)", cache->D);
+    if ((rc = check_rows("rkv_prompt_attn: q", cache, q, q_stride, cache->Hq))) return rc;
+    if ((rc = check_rows("rkv_prompt_attn: k", cache, k, k_stride, cache->H))) return rc;
+    if ((rc = check_rows("rkv_prompt_attn: v", cache, v, v_stride, cache->H))) return rc;
+    if ((rc = check_rows("rkv_prompt_attn: out", cache, out, out_stride, cache->Hq))) return rc;
+    WsLayout L;
+    if ((rc = check_ws(cache, ws, ws_bytes, &L))) return rc;
+    PromptArgs a{};
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.out_stride = out_stride;
+    a.cu = cu;
+    a.out = out;
+    a.lse = lse;
+    a.status = at<int32_t>(ws, L.status);
+    a.B = cache->B;
+    a.H = cache->H;
+    a.Hq = cache->Hq;
+    a.n_tokens = n_tokens;
+    a.qscale = scale * 1.4426950408889634f;
+    cudaError_t e = launch_prompt(a, cache->dtype, cache->D, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "rkv_prompt_attn");
+    return RKV_OK;
+}
+
+RKV_API size_t rkv_tree_workspace_size(const rkv_cache_t *cache, int32_t max_nodes) {
+    if (check_cache(cache, false) != RKV_OK) return 0;
+    if (max_nodes < 1 || max_nodes > TREE_MAX_NODES) {
+        fail(RKV_ERR_INVALID_ARG, "max_nodes must be in [1, %d]", TREE_MAX_NODES);
+        return 0;
+    }
+    size_t ticket, rec, total;
+    tree_offsets(*cache, max_nodes, &ticket, &rec, &total);
+    return total;
+}
+
+RKV_API int rkv_tree_attn(const rkv_cache_t *cache, const int32_t *cu, int32_t n_tokens, int32_t max_nodes,
+                          const void *q, const void *k_draft, const void *v_draft, const uint64_t *mask, float scale,
+                          const rkv_select_t *sel, void *out, float *lse, void *ws, size_t ws_bytes, void *stream) {
+    const NvtxRange nvtx_range("rkv_tree_attn");
+    int rc = check_cache(cache, true);
+    if (rc) return rc;
+    if ((rc = check_packed("rkv_tree_attn", cache, cu, n_tokens))) return rc;
+    if (max_nodes < 1 || max_nodes > TREE_MAX_NODES)
+        return fail(RKV_ERR_INVALID_ARG, "rkv_tree_attn: max_nodes must be in [1, %d]", TREE_MAX_NODES);
+    if (!q || !k_draft || !v_draft || !mask || !out)
+        return fail(RKV_ERR_INVALID_ARG, "rkv_tree_attn: q, k_draft, v_draft, mask and out must be non-NULL");
+    if (!aligned16(q) || !aligned16(k_draft) || !aligned16(v_draft) || !aligned16(out))
+        return fail(RKV_ERR_INVALID_ARG, "rkv_tree_attn: q, k_draft, v_draft and out must be 16-byte aligned");
+    if (sel && !sel->keep_mask) return fail(RKV_ERR_INVALID_ARG, "rkv_tree_attn: sel->keep_mask is NULL");
+    if (cache->D != 64 && cache->D != 128)
+        return fail(RKV_ERR_UNSUPPORTED, "rkv_tree_attn: D = %d is not built (64 or 128)", cache->D);
+    const int G = cache->Hq / cache->H;
+    if (G > TREE_MAX_G) return fail(RKV_ERR_UNSUPPORTED, "rkv_tree_attn: more than %d query heads per KV head", TREE_MAX_G);
+    WsLayout L;
+    if ((rc = check_ws(cache, ws, ws_bytes, &L))) return rc;
+    size_t ticket, rec, total;
+    const TreeLayout tl = tree_offsets(*cache, max_nodes, &ticket, &rec, &total);
+    if (ws_bytes < total)
+        return fail(RKV_ERR_WORKSPACE_TOO_SMALL, "workspace of %zu bytes < %zu needed (rkv_tree_workspace_size)",
+                    ws_bytes, total);
+    TreeArgs a{};
+    a.k_pool = cache->k_pool;
+    a.v_pool = cache->v_pool;
+    a.block_table = cache->block_table;
+    a.len = cache->len;
+    a.keep_mask = sel ? sel->keep_mask : nullptr;
+    a.cu = cu;
+    a.q = q;
+    a.k_draft = k_draft;
+    a.v_draft = v_draft;
+    a.mask = reinterpret_cast<const unsigned long long *>(mask);
+    a.out = out;
+    a.lse = lse;
+    a.status = at<int32_t>(ws, L.status);
+    a.ticket = at<uint32_t>(ws, ticket);
+    a.rec = at<float>(ws, rec);
+    a.B = cache->B;
+    a.LH = cache->L * cache->H;
+    a.G = G;
+    a.C = cache->B * a.LH;
+    a.max_pages = cache->max_pages;
+    a.n_pages = cache->n_pages;
+    a.n_tokens = n_tokens;
+    a.max_nodes = max_nodes;
+    a.row_tiles = tl.row_tiles;
+    a.parts = tl.parts;
+    a.qscale = scale * 1.4426950408889634f;
+    cudaError_t e = launch_tree(a, cache->dtype, cache->D, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "rkv_tree_attn");
+    return RKV_OK;
+}
+
+RKV_API int rkv_append_tokens(const rkv_cache_t *cache, const int32_t *cu, const int32_t *tok, int32_t n_new,
+                              const int32_t *pos0, const void *k_new, const void *v_new, const float *lb_new,
+                              int32_t n_rows, void *ws, size_t ws_bytes, void *stream) {
+    const NvtxRange nvtx_range("rkv_append_tokens");
+    int rc = check_cache(cache, true);
+    if (rc) return rc;
+    if ((rc = check_packed("rkv_append_tokens", cache, cu, n_new))) return rc;
+    if (!pos0 || !k_new || !v_new || !lb_new) return fail(RKV_ERR_INVALID_ARG, "rkv_append_tokens: an input is NULL");
+    if (!aligned16(k_new) || !aligned16(v_new))
+        return fail(RKV_ERR_INVALID_ARG, "rkv_append_tokens: k_new / v_new must be 16-byte aligned");
+    if (n_rows < 1 || (!tok && n_rows < n_new))
+        return fail(RKV_ERR_INVALID_ARG, "rkv_append_tokens: n_rows (%d) must be positive, and without tok at least "
+                                         "n_new (%d)", n_rows, n_new);
+    if ((rc = check_moved("rkv_append_tokens", cache))) return rc;
+    WsLayout L;
+    if ((rc = check_ws(cache, ws, ws_bytes, &L))) return rc;
+    AppendTokensArgs a{};
+    a.k_pool = cache->k_pool;
+    a.v_pool = cache->v_pool;
+    a.pos_pool = cache->pos_pool;
+    a.lb_pool = cache->lb_pool;
+    a.block_table = cache->block_table;
+    a.len = cache->len;
+    a.free_stack = cache->free_stack;
+    a.free_top = cache->free_top;
+    a.cu = cu;
+    a.tok = tok;
+    a.pos0 = pos0;
+    a.k_new = k_new;
+    a.v_new = v_new;
+    a.lb_new = lb_new;
+    a.status = at<int32_t>(ws, L.status);
+    a.plan = at<int32_t>(ws, L.seq_plan);
+    a.base = at<int32_t>(ws, L.seq_base);
+    a.pop = at<int32_t>(ws, L.seq_pop);
+    a.B = cache->B;
+    a.LH = cache->L * cache->H;
+    a.C = cache->B * a.LH;
+    a.max_pages = cache->max_pages;
+    a.n_pages = cache->n_pages;
+    a.n_new = n_new;
+    a.n_rows = n_rows;
+    cudaError_t e = launch_append_tokens(a, cache->D * elt_bytes(cache->dtype), static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "rkv_append_tokens");
+    return RKV_OK;
+}
+
+RKV_API int rkv_fork_sequences(const rkv_cache_t *cache, const int32_t *parent, void *ws, size_t ws_bytes,
+                               void *stream) {
+    const NvtxRange nvtx_range("rkv_fork_sequences");
+    int rc = check_cache(cache, true);
+    if (rc) return rc;
+    if (!parent) return fail(RKV_ERR_INVALID_ARG, "rkv_fork_sequences: parent is NULL");
+    if (cache->B > FORK_MAX_B)
+        return fail(RKV_ERR_UNSUPPORTED, "rkv_fork_sequences: at most %d sequences", FORK_MAX_B);
+    if ((rc = check_moved("rkv_fork_sequences", cache))) return rc;
+    WsLayout L;
+    if ((rc = check_ws(cache, ws, ws_bytes, &L))) return rc;
+    ForkArgs a{};
+    a.k_pool = cache->k_pool;
+    a.v_pool = cache->v_pool;
+    a.pos_pool = cache->pos_pool;
+    a.lb_pool = cache->lb_pool;
+    a.block_table = cache->block_table;
+    a.len = cache->len;
+    a.free_stack = cache->free_stack;
+    a.free_top = cache->free_top;
+    a.parent = parent;
+    a.status = at<int32_t>(ws, L.status);
+    a.plan = at<int32_t>(ws, L.seq_plan);
+    a.base = at<int32_t>(ws, L.seq_base);
+    a.pop = at<int32_t>(ws, L.seq_pop);
+    a.B = cache->B;
+    a.LH = cache->L * cache->H;
+    a.C = cache->B * a.LH;
+    a.max_pages = cache->max_pages;
+    a.n_pages = cache->n_pages;
+    cudaError_t e = launch_fork(a, cache->D * elt_bytes(cache->dtype), static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "rkv_fork_sequences");
     return RKV_OK;
 }
 

@@ -46,6 +46,9 @@ struct WsLayout {
     size_t bfloor;        // int32  [C] oldest floor position (ContourKV)
     size_t bskip;         // uint8  [C] flat heads (ContourKV)
     size_t bseq;          // uint64 [B][2] forced entries, entries left to rank (ContourKV)
+    size_t seq_plan;      // int32 [2] outcome of a sequence plan: go, free pages after it
+    size_t seq_base;      // int32 [C] lengths a sequence operator works from
+    size_t seq_pop;       // int32 [C] stack index of the first page each head takes
     size_t total;
 };
 
@@ -304,5 +307,77 @@ struct AppendArgs {
     int C, LH, max_pages, row_bytes;
 };
 cudaError_t launch_append(const AppendArgs &a, cudaStream_t s);
+
+// Prompt attention (prompt.cu).
+constexpr int SERVE_MAX_B = 1024;   // sequences per call of the packed operators
+struct PromptArgs {
+    const void *q, *k, *v;     // [n_tokens][heads][D], token strides in elements
+    int64_t q_stride, k_stride, v_stride, out_stride;
+    const int32_t *cu;         // [B+1]
+    void *out;
+    float *lse;                // [n_tokens][Hq], may be NULL
+    int32_t *status;
+    int B, H, Hq, n_tokens;
+    float qscale;              // scale * log2(e)
+};
+cudaError_t launch_prompt(const PromptArgs &a, int dtype, int D, cudaStream_t s);
+
+// Tree attention (tree.cu).
+constexpr int TREE_MAX_NODES = 64;  // a node's mask is one 64-bit word
+constexpr int TREE_MAX_G = 64;
+struct TreeArgs {
+    const void *k_pool, *v_pool;
+    const int32_t *block_table;
+    const int32_t *len;
+    const uint16_t *keep_mask; // NULL: every entry kept
+    const int32_t *cu;         // [B+1]
+    const void *q;             // [n_tokens][L][Hq][D]
+    const void *k_draft, *v_draft;  // [n_tokens][L][H][D]
+    const unsigned long long *mask; // [n_tokens]
+    void *out;                 // [n_tokens][L][Hq][D]
+    float *lse;                // may be NULL
+    int32_t *status;
+    uint32_t *ticket;          // self-resetting
+    float *rec;
+    int B, LH, G, C, max_pages, n_pages, n_tokens, max_nodes;
+    int row_tiles, parts;
+    float qscale;
+};
+// The workspace's part for trees of up to max_nodes tokens.
+struct TreeLayout {
+    int row_tiles, parts;
+    size_t tickets;            // uint32
+    size_t rec_floats;
+};
+TreeLayout tree_layout(int dtype, int D, int G, int64_t C, int max_nodes);
+cudaError_t launch_tree(const TreeArgs &a, int dtype, int D, cudaStream_t s);
+
+// Whole sequences (sequences.cu).
+struct AppendTokensArgs {
+    void *k_pool, *v_pool;
+    int32_t *pos_pool;
+    float *lb_pool;
+    int32_t *block_table, *len, *free_stack, *free_top;
+    const int32_t *cu;         // [B+1]
+    const int32_t *tok;        // rows to append, NULL: rows in order
+    const int32_t *pos0;       // [B]
+    const void *k_new, *v_new; // [n_rows][L*H][D]
+    const float *lb_new;       // [n_rows][L*H]
+    int32_t *status, *plan, *base, *pop;
+    int B, LH, C, max_pages, n_pages, n_new, n_rows;
+};
+cudaError_t launch_append_tokens(const AppendTokensArgs &a, int row_bytes, cudaStream_t s);
+
+constexpr int FORK_MAX_B = 64;
+struct ForkArgs {
+    void *k_pool, *v_pool;
+    int32_t *pos_pool;
+    float *lb_pool;
+    int32_t *block_table, *len, *free_stack, *free_top;
+    const int32_t *parent;     // [B]
+    int32_t *status, *plan, *base, *pop;
+    int B, LH, C, max_pages, n_pages;
+};
+cudaError_t launch_fork(const ForkArgs &a, int row_bytes, cudaStream_t s);
 
 }  // namespace rkv

@@ -1,0 +1,95 @@
+// prompt.cu -- rkv_prompt_attn: causal grouped-query attention over the
+// packed prompts of a batch (one layer a call).
+//
+//   o[i] = sum_{j <= i} exp(z_ij - lse_i) v_j,  z_ij = scale <q_i, k_j>,
+//   lse_i = log sum_{j <= i} exp(z_ij)
+#include "internal.h"
+#include "serve.cuh"
+
+namespace rkv {
+namespace {
+
+// One CTA per (64 query rows, query head): FFMA products, see serve.cuh.
+template <typename T, int D>
+__global__ void __launch_bounds__(FT_THREADS) prompt_ffma_kernel(const PromptArgs a) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    FTile<D> &t = *reinterpret_cast<FTile<D> *>(smem);
+    int32_t *s_cu = reinterpret_cast<int32_t *>(smem + sizeof(FTile<D>));
+    __shared__ SeqTile s_tile;
+    if (!load_offsets(a.cu, a.B, a.n_tokens, a.n_tokens, s_cu, a.status)) return;
+    const int tile = blockIdx.x / a.Hq, hq = blockIdx.x % a.Hq;
+    if (threadIdx.x < 32) {
+        SeqTile w{-1, 0};
+        if (tile < tiles_from(s_cu, a.B, FT_ROWS, 0)) w = find_tile(s_cu, a.B, a.n_tokens, FT_ROWS, tile);
+        if (threadIdx.x == 0) s_tile = w;
+    }
+    __syncthreads();
+    const SeqTile w = s_tile;
+    if (w.b < 0) return;
+    const int64_t t0 = s_cu[w.b];
+    const int n = s_cu[w.b + 1] - s_cu[w.b], r0 = w.blk * FT_ROWS, h = hq / (a.Hq / a.H);
+    const T *q = static_cast<const T *>(a.q) + (int64_t)hq * D;
+    const T *k = static_cast<const T *>(a.k) + (int64_t)h * D;
+    const T *v = static_cast<const T *>(a.v) + (int64_t)h * D;
+    constexpr int V4 = D / 4;
+    for (int i = threadIdx.x; i < FT_ROWS * V4; i += FT_THREADS) {
+        const int r = i / V4, d = i % V4 * 4;
+        const float4 x = r0 + r < n ? ld4(q + (t0 + r0 + r) * a.q_stride + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+        *reinterpret_cast<float4 *>(&t.q[r][d]) = x;
+    }
+    FState<D> st;
+    st.init();
+    const int last = min(r0 + FT_ROWS, n);
+    for (int j0 = 0; j0 < last; j0 += FT_KEYS) {
+        __syncthreads();
+        int odd = 0;
+        for (int i = threadIdx.x; i < FT_KEYS * V4; i += FT_THREADS) {
+            const int r = i / V4, d = i % V4 * 4;
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+            if (j0 + r < n) {
+                x = ld4(k + (t0 + j0 + r) * a.k_stride + d);
+                y = ld4(v + (t0 + j0 + r) * a.v_stride + d);
+                odd |= odd4(y);
+            }
+            *reinterpret_cast<float4 *>(&t.k[r][d]) = x;
+            *reinterpret_cast<float4 *>(&t.v[r][d]) = y;
+        }
+        odd = __syncthreads_or(odd);
+        ftile_step<D>(t, st, a.qscale, j0 + FT_KEYS > r0, odd != 0,
+                      [&](int row, int key) { return j0 + key > r0 + row; });
+    }
+    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const int r = r0 + ty * 4 + i;
+        if (r >= n) continue;
+        T *o = static_cast<T *>(a.out) + (t0 + r) * a.out_stride + (int64_t)hq * D;
+        const float inv = 1.f / st.l[i];
+#pragma unroll
+        for (int j = 0; j < D / 64; j++)
+            st4(o + tx * 4 + 64 * j, make_float4(st.o[i][4 * j] * inv, st.o[i][4 * j + 1] * inv,
+                                                 st.o[i][4 * j + 2] * inv, st.o[i][4 * j + 3] * inv));
+        if (a.lse && tx == 0) a.lse[(t0 + r) * a.Hq + hq] = (st.m[i] + log2f(st.l[i])) * LN2;
+    }
+}
+
+template <typename T, int D>
+cudaError_t launch_ffma(const PromptArgs &a, cudaStream_t s) {
+    const size_t smem = sizeof(FTile<D>) + (size_t)(a.B + 1) * 4;
+    cudaError_t e = cudaFuncSetAttribute(prompt_ffma_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)smem);
+    if (e != cudaSuccess) return e;
+    const int64_t tiles = (int64_t)(a.n_tokens / FT_ROWS + a.B) * a.Hq;
+    if (tiles >= (1ll << 31)) return cudaErrorNotSupported;
+    prompt_ffma_kernel<T, D><<<(unsigned)tiles, FT_THREADS, smem, s>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_prompt(const PromptArgs &a, int dtype, int D, cudaStream_t s) {
+    if (dtype == RKV_BF16) return D == 64 ? launch_ffma<__nv_bfloat16, 64>(a, s) : launch_ffma<__nv_bfloat16, 128>(a, s);
+    return D == 64 ? launch_ffma<float, 64>(a, s) : launch_ffma<float, 128>(a, s);
+}
+
+}  // namespace rkv

@@ -1,0 +1,330 @@
+// sequences.cu -- whole sequences in the paged cache: rkv_append_tokens (many
+// tokens per sequence) and rkv_fork_sequences (copying, moving and freeing).
+// Both move bytes; each is a plan launch (one scan over the heads decides
+// which pages are taken and given back) and a launch that moves the rows.
+#include "internal.h"
+#include "serve.cuh"
+
+namespace rkv {
+namespace {
+
+constexpr int PLAN_THREADS = 1024;
+
+__device__ __forceinline__ int pages_of(int n) { return (n + PAGE - 1) / PAGE; }
+
+// ---------------------------------------------------------------- append ----
+// Plan: head c needs pages_of(len + n) - pages_of(len) new pages; heads pop in
+// ascending order.  base[c] = its length before the call (-1: the head takes
+// nothing), pop[c] = index of its first page on the free stack (later ones
+// below it).  A head that would leave its table takes no page; one that finds
+// too few pages is skipped, and so is every later head that needs one.
+__global__ void __launch_bounds__(PLAN_THREADS) append_plan_kernel(const AppendTokensArgs a) {
+    extern __shared__ int32_t s_cu[];
+    __shared__ uint32_t scan[33];
+    __shared__ int s_short;
+    if (threadIdx.x == 0) {
+        s_short = INT32_MAX;
+        a.plan[0] = 0;
+    }
+    if (!load_offsets(a.cu, a.B, a.n_new, a.n_new, s_cu, a.status)) return;
+    const int top = min(max(*a.free_top, 0), a.n_pages);
+    uint32_t taken = 0;
+    for (int c0 = 0; c0 < a.C; c0 += PLAN_THREADS) {
+        const int c = c0 + threadIdx.x;
+        int len = 0, n = 0, need = 0, bits = 0;
+        if (c < a.C) {
+            const int b = c / a.LH;
+            n = s_cu[b + 1] - s_cu[b];
+            len = a.len[c];
+            if (len < 0) bits = RKV_DEV_BAD_INPUT;
+            else if ((int64_t)len + n > (int64_t)a.max_pages * PAGE) bits = RKV_DEV_TABLE_OVERFLOW;
+            const int32_t p0 = __ldg(a.pos0 + b);
+            if (n > 0 && (p0 < 0 || (int64_t)p0 + n > INT32_MAX)) bits = RKV_DEV_BAD_INPUT;
+            if (n == 0) bits = 0;
+            if (!bits) need = pages_of(len + n) - pages_of(len);
+        }
+        uint32_t total;
+        const uint32_t before = taken + block_exclusive_scan((uint32_t)need, scan, &total);
+        if (need > 0 && (int64_t)before + need > (int64_t)top) {
+            bits = RKV_DEV_POOL_EXHAUSTED;
+            atomicMin(&s_short, (int)before);  // pages taken by the heads before the first that fails
+        }
+        if (c < a.C) {
+            const bool ok = !bits && n > 0;
+            a.base[c] = ok ? len : -1;
+            a.pop[c] = top - 1 - (int)before;
+            if (ok) a.len[c] = len + n;
+            if (bits) set_status(a.status, bits);
+        }
+        taken += total;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        *a.free_top = top - (int)min((uint32_t)s_short, taken);
+        a.plan[0] = 1;
+    }
+}
+
+// Rows of all heads in order (head, token): a warp takes 32 of them.  Lane i
+// finds where row i goes (its page is in the table, or the head's next one on
+// the stack, which is then entered in the table); the warp then copies the 32
+// K and V rows in 16-byte pieces.
+constexpr int MOVE_THREADS = 256;
+template <int CH>  // 16-byte pieces of a row
+__global__ void __launch_bounds__(MOVE_THREADS) append_rows_kernel(const AppendTokensArgs a) {
+    extern __shared__ int32_t s_cu[];
+    if (a.plan[0] == 0) return;
+    for (int i = threadIdx.x; i <= a.B; i += MOVE_THREADS) s_cu[i] = __ldg(a.cu + i);
+    __syncthreads();
+    const int lane = threadIdx.x & 31;
+    const int64_t warps = (int64_t)gridDim.x * (MOVE_THREADS / 32);
+    const int64_t rows = (int64_t)(s_cu[a.B] - s_cu[0]) * a.LH;
+    int b = 0;
+    for (int64_t g = ((int64_t)blockIdx.x * (MOVE_THREADS / 32) + (threadIdx.x >> 5)) * 32; g < rows; g += warps * 32) {
+        const int64_t i = g + lane;
+        int64_t dst = -1, src = 0;
+        if (i < rows) {
+            while ((int64_t)(s_cu[b + 1] - s_cu[0]) * a.LH <= i) b++;
+            const int64_t r = i - (int64_t)(s_cu[b] - s_cu[0]) * a.LH;
+            const int n = s_cu[b + 1] - s_cu[b], lh = (int)(r / n), j = (int)(r % n);
+            const int c = b * a.LH + lh, base = a.base[c];
+            int64_t row = s_cu[b] + j;
+            if (a.tok) row = __ldg(a.tok + row);
+            if (base >= 0) {
+                const int slot = base + j, p = slot / PAGE, have = pages_of(base);
+                int32_t *entry = a.block_table + (int64_t)c * a.max_pages + p;
+                const int32_t page = p < have ? *entry : a.free_stack[a.pop[c] - (p - have)];
+                if (p >= have && slot % PAGE == 0) *entry = page;
+                if (page < 0 || page >= a.n_pages || row < 0 || row >= a.n_rows) {
+                    set_status(a.status, RKV_DEV_BAD_INPUT);
+                } else {
+                    src = row * a.LH + lh;
+                    dst = (int64_t)page * PAGE + slot % PAGE;
+                    a.pos_pool[dst] = __ldg(a.pos0 + b) + j;
+                    a.lb_pool[dst] = __ldg(a.lb_new + src);
+                }
+            }
+        }
+        constexpr int PER = 32 / CH, UN = 8;  // rows a warp moves at once, steps in flight
+#pragma unroll 1
+        for (int k0 = 0; k0 < 32; k0 += PER * UN) {
+            uint4 xk[UN], xv[UN];
+            int64_t to[UN];
+#pragma unroll
+            for (int u = 0; u < UN; u++) {
+                const int k = (k0 + u * PER + lane / CH) & 31;
+                to[u] = __shfl_sync(0xFFFFFFFFu, dst, k);
+                const int64_t from = __shfl_sync(0xFFFFFFFFu, src, k);
+                if (to[u] >= 0) {
+                    xk[u] = __ldcs(static_cast<const uint4 *>(a.k_new) + from * CH + lane % CH);
+                    xv[u] = __ldcs(static_cast<const uint4 *>(a.v_new) + from * CH + lane % CH);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < UN; u++)
+                if (to[u] >= 0) {
+                    static_cast<uint4 *>(a.k_pool)[to[u] * CH + lane % CH] = xk[u];
+                    static_cast<uint4 *>(a.v_pool)[to[u] * CH + lane % CH] = xv[u];
+                }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ fork ----
+// The slot that goes on with a sequence's own pages: the sequence's slot
+// itself if it continues it, else the first slot that does.
+__device__ __forceinline__ int heir_of(const int32_t *parent, int B, int s) {
+    if (parent[s] == s) return s;
+    for (int b = 0; b < B; b++)
+        if (parent[b] == s) return b;
+    return -1;
+}
+
+// Plan of the fork, and the pages of ended sequences pushed onto the stack.
+// Every CTA scans all heads (how many pages each gives back and takes) and
+// pushes the pages of its own share of them; CTA 0 writes the plan.
+__global__ void __launch_bounds__(PLAN_THREADS) fork_plan_kernel(const ForkArgs a) {
+    __shared__ int32_t s_par[FORK_MAX_B], s_heir[FORK_MAX_B];
+    __shared__ uint32_t scan[33];
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.plan[0] = 0;
+    int bad = 0;
+    if (threadIdx.x < a.B) {
+        const int32_t p = __ldg(a.parent + threadIdx.x);
+        s_par[threadIdx.x] = p;
+        bad = p < -1 || p >= a.B;
+    }
+    bad = __syncthreads_or(bad);
+    if (bad) {
+        if (threadIdx.x == 0) set_status(a.status, RKV_DEV_BAD_INPUT);
+        return;
+    }
+    if (threadIdx.x < a.B) s_heir[threadIdx.x] = heir_of(s_par, a.B, threadIdx.x);
+    __syncthreads();
+    const int top = min(max(*a.free_top, 0), a.n_pages);
+    uint32_t gives = 0, takes = 0;
+    for (int pass = 0; pass < 2; pass++) {
+        // first the totals, then (if the stack holds enough) the pushes and the plan
+        if (pass == 1 && (int64_t)top + gives - takes < 0) {
+            if (threadIdx.x == 0) set_status(a.status, RKV_DEV_POOL_EXHAUSTED);
+            return;
+        }
+        uint32_t given = 0, taken = 0;
+        for (int c0 = 0; c0 < a.C; c0 += PLAN_THREADS) {
+            const int c = c0 + threadIdx.x;
+            int give = 0, take = 0, n = 0;
+            if (c < a.C) {
+                const int b = c / a.LH, lh = c % a.LH, p = s_par[b];
+                if (s_heir[b] < 0) give = pages_of(clamp_len(a.len[c], a.max_pages, a.status));
+                if (p >= 0) {
+                    n = clamp_len(a.len[p * a.LH + lh], a.max_pages, a.status);
+                    if (s_heir[p] != b) take = pages_of(n);
+                }
+            }
+            uint32_t tg, tt;
+            const uint32_t g0 = given + block_exclusive_scan((uint32_t)give, scan, &tg);
+            const uint32_t t0 = taken + block_exclusive_scan((uint32_t)take, scan, &tt);
+            given += tg;
+            taken += tt;
+            if (pass == 1 && c < a.C) {
+                if (blockIdx.x == 0) {
+                    a.base[c] = n;
+                    a.pop[c] = top + (int)gives - 1 - (int)t0;
+                }
+                // CTAs take the heads in turn, so that those of one ended sequence spread
+                if (c % (int)gridDim.x == (int)blockIdx.x)
+                    for (int k = 0; k < give && top + (int)g0 + k < a.n_pages; k++)
+                        a.free_stack[top + (int)g0 + k] = a.block_table[(int64_t)c * a.max_pages + k];
+            }
+        }
+        gives = given;
+        takes = taken;
+    }
+    __syncthreads();
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        a.plan[1] = top + (int)gives - (int)takes;
+        a.plan[0] = 1;
+    }
+}
+
+// One CTA: FORK_COLS table indices of one (layer, head) over all slots.  The
+// old entries of the column are read first, then the new ones written, so
+// that slots may exchange their pages freely.  A page that several slots copy
+// is read once.
+constexpr int FORK_COLS = 8, FORK_THREADS = 256;
+template <int CH>
+__global__ void __launch_bounds__(FORK_THREADS) fork_rows_kernel(const ForkArgs a) {
+    __shared__ int32_t s_par[FORK_MAX_B], s_heir[FORK_MAX_B], s_n[FORK_MAX_B], s_pop[FORK_MAX_B];
+    __shared__ int32_t s_old[FORK_MAX_B][FORK_COLS], s_new[FORK_MAX_B][FORK_COLS];
+    if (a.plan[0] == 0) return;
+    const int blocks = (a.max_pages + FORK_COLS - 1) / FORK_COLS;
+    const int lh = blockIdx.x / blocks, p0 = blockIdx.x % blocks * FORK_COLS;
+    if (threadIdx.x < a.B) {
+        s_par[threadIdx.x] = __ldg(a.parent + threadIdx.x);
+        s_n[threadIdx.x] = a.base[threadIdx.x * a.LH + lh];
+        s_pop[threadIdx.x] = a.pop[threadIdx.x * a.LH + lh];
+    }
+    __syncthreads();
+    if (threadIdx.x < a.B) s_heir[threadIdx.x] = heir_of(s_par, a.B, threadIdx.x);
+    for (int i = threadIdx.x; i < a.B * FORK_COLS; i += FORK_THREADS) {
+        const int b = i / FORK_COLS, p = p0 + i % FORK_COLS;
+        s_old[b][i % FORK_COLS] = p < a.max_pages ? a.block_table[((int64_t)b * a.LH + lh) * a.max_pages + p] : -1;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.B * FORK_COLS; i += FORK_THREADS) {
+        const int b = i / FORK_COLS, k = i % FORK_COLS, p = p0 + k, s = s_par[b];
+        int32_t page = -1;
+        if (s >= 0 && p < pages_of(s_n[b])) page = s_heir[s] == b ? s_old[s][k] : a.free_stack[s_pop[b] - p];
+        s_new[b][k] = page;
+        if (p < a.max_pages && page != s_old[b][k]) a.block_table[((int64_t)b * a.LH + lh) * a.max_pages + p] = page;
+        if (p == 0) a.len[b * a.LH + lh] = s_n[b];
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.free_top = a.plan[1];
+    __syncthreads();
+    // a warp per (source sequence, column): the page's rows to every slot that copies it
+    const int lane = threadIdx.x & 31;
+    for (int w = threadIdx.x >> 5; w < a.B * FORK_COLS; w += FORK_THREADS / 32) {
+        const int s = w / FORK_COLS, k = w % FORK_COLS, heir = s_heir[s];
+        if (heir < 0 || p0 + k >= pages_of(s_n[heir])) continue;
+        uint32_t lo = 0, hi = 0;  // slots that copy s
+        lo = __ballot_sync(0xFFFFFFFFu, lane < a.B && s_par[lane] == s && heir != lane);
+        hi = __ballot_sync(0xFFFFFFFFu, lane + 32 < a.B && s_par[lane + 32] == s && heir != lane + 32);
+        uint64_t to = (uint64_t)hi << 32 | lo;
+        if (!to) continue;
+        const int rows = min(PAGE, s_n[heir] - (p0 + k) * PAGE);
+        const int32_t from = s_old[s][k];
+        if (from < 0 || from >= a.n_pages) {
+            set_status(a.status, RKV_DEV_BAD_INPUT);
+            continue;
+        }
+        constexpr int UN = CH / 2;  // 16 rows of CH pieces over 32 lanes
+        uint4 xk[UN], xv[UN];
+        int32_t pos = 0;
+        float lb = 0.f;
+        const int64_t f0 = (int64_t)from * PAGE * CH;
+#pragma unroll
+        for (int u = 0; u < UN; u++)
+            if ((u * 32 + lane) / CH < rows) {
+                xk[u] = __ldcs(static_cast<const uint4 *>(a.k_pool) + f0 + u * 32 + lane);
+                xv[u] = __ldcs(static_cast<const uint4 *>(a.v_pool) + f0 + u * 32 + lane);
+            }
+        if (lane < rows) {
+            pos = a.pos_pool[(int64_t)from * PAGE + lane];
+            lb = a.lb_pool[(int64_t)from * PAGE + lane];
+        }
+        while (to) {
+            const int b = __ffsll((long long)to) - 1;
+            to &= to - 1;
+            const int32_t page = s_new[b][k];
+            if (page < 0 || page >= a.n_pages) {
+                set_status(a.status, RKV_DEV_BAD_INPUT);
+                continue;
+            }
+            const int64_t d0 = (int64_t)page * PAGE * CH;
+#pragma unroll
+            for (int u = 0; u < UN; u++)
+                if ((u * 32 + lane) / CH < rows) {
+                    static_cast<uint4 *>(a.k_pool)[d0 + u * 32 + lane] = xk[u];
+                    static_cast<uint4 *>(a.v_pool)[d0 + u * 32 + lane] = xv[u];
+                }
+            if (lane < rows) {
+                a.pos_pool[(int64_t)page * PAGE + lane] = pos;
+                a.lb_pool[(int64_t)page * PAGE + lane] = lb;
+            }
+        }
+    }
+}
+
+template <int CH>
+cudaError_t append_rows(const AppendTokensArgs &a, cudaStream_t s) {
+    const int64_t groups = ((int64_t)a.n_new * a.LH + 31) / 32, per = MOVE_THREADS / 32;
+    const int64_t ctas = (groups + per - 1) / per;
+    append_rows_kernel<CH><<<(unsigned)(ctas < 148 * 8 ? ctas : 148 * 8), MOVE_THREADS, (a.B + 1) * 4, s>>>(a);
+    return cudaGetLastError();
+}
+
+template <int CH>
+cudaError_t fork_rows(const ForkArgs &a, cudaStream_t s) {
+    const int64_t ctas = (int64_t)a.LH * ((a.max_pages + FORK_COLS - 1) / FORK_COLS);
+    if (ctas >= (1ll << 31)) return cudaErrorNotSupported;
+    fork_rows_kernel<CH><<<(unsigned)ctas, FORK_THREADS, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_append_tokens(const AppendTokensArgs &a, int row_bytes, cudaStream_t s) {
+    append_plan_kernel<<<1, PLAN_THREADS, (a.B + 1) * 4, s>>>(a);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return row_bytes == 128 ? append_rows<8>(a, s) : row_bytes == 256 ? append_rows<16>(a, s) : append_rows<32>(a, s);
+}
+
+cudaError_t launch_fork(const ForkArgs &a, int row_bytes, cudaStream_t s) {
+    const int64_t want = ((int64_t)a.C + 31) / 32;
+    fork_plan_kernel<<<(unsigned)(want < 148 ? want : 148), PLAN_THREADS, 0, s>>>(a);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return row_bytes == 128 ? fork_rows<8>(a, s) : row_bytes == 256 ? fork_rows<16>(a, s) : fork_rows<32>(a, s);
+}
+
+}  // namespace rkv

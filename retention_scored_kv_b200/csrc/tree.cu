@@ -1,0 +1,200 @@
+// tree.cu -- rkv_tree_attn: attention of a tree of drafted tokens over the
+// ragged paged cache.  Row (node i, query head g of the group) of KV head c
+// attends the head's kept cache entries and the drafted tokens j of its own
+// sequence with bit j of mask[i] set:
+//   o = sum_{kept cache} exp(z - lse) v + sum_{j in mask[i]} exp(z_j - lse) v_j
+#include "internal.h"
+#include "serve.cuh"
+
+namespace rkv {
+namespace {
+
+// What key a row of a key tile is.
+constexpr int32_t KEY_CACHE = -1, KEY_NONE = -2;  // >= 0: drafted token
+
+// One CTA per (head, 64 rows, part of the keys).  The keys of a head are its
+// cache pages and then its drafted tokens in groups of 16; a tile of 64 is four
+// of either.  Parts of one (head, rows) meet through records in the workspace:
+// the last to arrive joins them in ascending order, so the result does not
+// depend on which one that is.
+template <typename T, int D>
+__global__ void __launch_bounds__(FT_THREADS) tree_ffma_kernel(const TreeArgs a) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    FTile<D> &t = *reinterpret_cast<FTile<D> *>(smem);
+    int32_t *s_cu = reinterpret_cast<int32_t *>(smem + sizeof(FTile<D>));
+    __shared__ unsigned long long s_mask[64];
+    __shared__ int32_t s_key[FT_KEYS];
+    __shared__ const void *s_k[FT_KEYS], *s_v[FT_KEYS];
+    __shared__ int s_last;
+    if (!load_offsets(a.cu, a.B, a.n_tokens, a.max_nodes, s_cu, a.status)) return;
+    const int part = blockIdx.x % a.parts, item = blockIdx.x / a.parts;
+    const int c = item / a.row_tiles, r0 = item % a.row_tiles * FT_ROWS;
+    const int b = c / a.LH, lh = c % a.LH, G = a.G;
+    const int t0 = s_cu[b], nodes = s_cu[b + 1] - t0, R = nodes * G;
+    if (r0 >= R) return;
+    const int m = clamp_len(__ldg(a.len + c), a.max_pages, a.status);
+    const int np = (m + PAGE - 1) / PAGE, tiles = (np + (nodes + PAGE - 1) / PAGE + 3) / 4;
+    if (threadIdx.x < nodes) s_mask[threadIdx.x] = __ldg(a.mask + t0 + threadIdx.x);
+    constexpr int V4 = D / 4;
+    const T *q = static_cast<const T *>(a.q);
+    for (int i = threadIdx.x; i < FT_ROWS * V4; i += FT_THREADS) {
+        const int r = r0 + i / V4, d = i % V4 * 4;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < R) x = ld4(q + ((int64_t)(t0 + r / G) * a.LH * G + lh * G + r % G) * D + d);
+        *reinterpret_cast<float4 *>(&t.q[i / V4][d]) = x;
+    }
+    FState<D> st;
+    st.init();
+    const int last = (int)((int64_t)tiles * (part + 1) / a.parts);
+    for (int j0 = (int)((int64_t)tiles * part / a.parts); j0 < last; j0++) {
+        __syncthreads();
+        int some = 0;
+        if (threadIdx.x < FT_KEYS) {
+            const int u = j0 * 4 + threadIdx.x / PAGE, off = threadIdx.x % PAGE;
+            int32_t kind = KEY_NONE;
+            const T *kr = nullptr, *vr = nullptr;
+            if (u < np) {
+                const int32_t page = __ldg(a.block_table + (int64_t)c * a.max_pages + u);
+                const bool kept = !a.keep_mask || (__ldg(a.keep_mask + (int64_t)c * a.max_pages + u) >> off & 1);
+                if (page < 0 || page >= a.n_pages) {
+                    set_status(a.status, RKV_DEV_BAD_INPUT);
+                } else if (kept && u * PAGE + off < m) {
+                    kind = KEY_CACHE;
+                    kr = static_cast<const T *>(a.k_pool) + ((int64_t)page * PAGE + off) * D;
+                    vr = static_cast<const T *>(a.v_pool) + ((int64_t)page * PAGE + off) * D;
+                }
+            } else {
+                const int j = (u - np) * PAGE + off;
+                if (j < nodes) {
+                    kind = j;
+                    kr = static_cast<const T *>(a.k_draft) + ((int64_t)(t0 + j) * a.LH + lh) * D;
+                    vr = static_cast<const T *>(a.v_draft) + ((int64_t)(t0 + j) * a.LH + lh) * D;
+                }
+            }
+            some = kind != KEY_CACHE;
+            s_key[threadIdx.x] = kind;
+            s_k[threadIdx.x] = kr;
+            s_v[threadIdx.x] = vr;
+        }
+        some = __syncthreads_or(some);
+        int odd = 0;
+        for (int i = threadIdx.x; i < FT_KEYS * V4; i += FT_THREADS) {
+            const int r = i / V4, d = i % V4 * 4;
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+            if (s_k[r]) {
+                x = ld4(static_cast<const T *>(s_k[r]) + d);
+                y = ld4(static_cast<const T *>(s_v[r]) + d);
+                odd |= odd4(y);
+            }
+            *reinterpret_cast<float4 *>(&t.k[r][d]) = x;
+            *reinterpret_cast<float4 *>(&t.v[r][d]) = y;
+        }
+        odd = __syncthreads_or(odd);
+        ftile_step<D>(t, st, a.qscale, some != 0, odd != 0, [&](int row, int key) {
+            const int32_t kind = s_key[key];
+            if (kind == KEY_CACHE) return false;
+            const int node = (r0 + row) / G;
+            return kind == KEY_NONE || node >= nodes || !(s_mask[node] >> kind & 1ull);
+        });
+    }
+    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+    constexpr int REC = FT_ROWS * (D + 2);  // per part: output sums, then maxima and sums
+    if (a.parts > 1) {
+        float *rec = a.rec + ((int64_t)item * a.parts + part) * REC;
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const int r = ty * 4 + i;
+#pragma unroll
+            for (int j = 0; j < D / 64; j++)
+                st4(rec + r * D + tx * 4 + 64 * j, make_float4(st.o[i][4 * j], st.o[i][4 * j + 1], st.o[i][4 * j + 2],
+                                                               st.o[i][4 * j + 3]));
+            if (tx == 0) {
+                rec[FT_ROWS * D + r] = st.m[i];
+                rec[FT_ROWS * D + FT_ROWS + r] = st.l[i];
+            }
+        }
+        __threadfence();
+        __syncthreads();
+        if (threadIdx.x == 0) s_last = atomicAdd(a.ticket + item, 1u) == (uint32_t)a.parts - 1u;
+        __syncthreads();
+        if (!s_last) return;
+        __threadfence();
+        if (threadIdx.x == 0) a.ticket[item] = 0u;
+        st.init();
+        for (int p = 0; p < a.parts; p++) {
+            const float *rp = a.rec + ((int64_t)item * a.parts + p) * REC;
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const int r = ty * 4 + i;
+                const float mp = __ldcg(rp + FT_ROWS * D + r), lp = __ldcg(rp + FT_ROWS * D + FT_ROWS + r);
+                const float mn = fmaxf(st.m[i], mp), ms = mn == -INFINITY ? 0.f : mn;
+                const float f = exp2f(st.m[i] - ms), g = exp2f(mp - ms);
+                st.m[i] = mn;
+                st.l[i] = st.l[i] * f + lp * g;
+#pragma unroll
+                for (int j = 0; j < D / 64; j++) {
+                    const float4 x = __ldcg(reinterpret_cast<const float4 *>(rp + r * D + tx * 4 + 64 * j));
+                    st.o[i][4 * j + 0] = st.o[i][4 * j + 0] * f + x.x * g;
+                    st.o[i][4 * j + 1] = st.o[i][4 * j + 1] * f + x.y * g;
+                    st.o[i][4 * j + 2] = st.o[i][4 * j + 2] * f + x.z * g;
+                    st.o[i][4 * j + 3] = st.o[i][4 * j + 3] * f + x.w * g;
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const int r = r0 + ty * 4 + i;
+        if (r >= R) continue;
+        const int64_t at = (int64_t)(t0 + r / G) * a.LH * G + lh * G + r % G;
+        T *o = static_cast<T *>(a.out) + at * D;
+        const bool none = st.m[i] == -INFINITY && st.l[i] == 0.f;
+        const float inv = none ? 0.f : 1.f / st.l[i];
+#pragma unroll
+        for (int j = 0; j < D / 64; j++)
+            st4(o + tx * 4 + 64 * j, make_float4(st.o[i][4 * j] * inv, st.o[i][4 * j + 1] * inv,
+                                                 st.o[i][4 * j + 2] * inv, st.o[i][4 * j + 3] * inv));
+        if (a.lse && tx == 0) a.lse[at] = none ? -INFINITY : (st.m[i] + log2f(st.l[i])) * LN2;
+    }
+}
+
+template <typename T, int D>
+cudaError_t launch_ffma(const TreeArgs &a, cudaStream_t s) {
+    const size_t smem = sizeof(FTile<D>) + (size_t)(a.B + 1) * 4;
+    cudaError_t e = cudaFuncSetAttribute(tree_ffma_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)smem);
+    if (e != cudaSuccess) return e;
+    const int64_t ctas = (int64_t)a.C * a.row_tiles * a.parts;
+    if (ctas >= (1ll << 31)) return cudaErrorNotSupported;
+    tree_ffma_kernel<T, D><<<(unsigned)ctas, FT_THREADS, smem, s>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+// Parts of each (head, 64 rows): enough for two CTAs on each of the 148 SMs
+// when there are few of them, up to 16.
+static int ffma_parts(int64_t items) {
+    const int64_t p = (295 + items) / items;
+    return (int)(p > 16 ? 16 : p);
+}
+
+TreeLayout tree_layout(int dtype, int D, int G, int64_t C, int max_nodes) {
+    (void)dtype;
+    TreeLayout L{};
+    L.row_tiles = (max_nodes * G + FT_ROWS - 1) / FT_ROWS;
+    const int64_t items = C * L.row_tiles;
+    L.parts = ffma_parts(items);
+    // as many for every max_nodes: calls of different sizes share a workspace,
+    // and a record of one must not land on another's (zeroed) tickets
+    L.tickets = (size_t)C * ((TREE_MAX_NODES * G + FT_ROWS - 1) / FT_ROWS);
+    L.rec_floats = L.parts > 1 ? (size_t)items * L.parts * FT_ROWS * (D + 2) : 0;
+    return L;
+}
+
+cudaError_t launch_tree(const TreeArgs &a, int dtype, int D, cudaStream_t s) {
+    if (dtype == RKV_BF16) return D == 64 ? launch_ffma<__nv_bfloat16, 64>(a, s) : launch_ffma<__nv_bfloat16, 128>(a, s);
+    return D == 64 ? launch_ffma<float, 64>(a, s) : launch_ffma<float, 128>(a, s);
+}
+
+}  // namespace rkv
