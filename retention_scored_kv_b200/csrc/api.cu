@@ -120,6 +120,7 @@ void layout_for(const rkv_cache_t &c, int sel_groups_x_waves, WsLayout *L) {
     L->bfloor = take((size_t)C * 4, 256);
     L->bskip = take((size_t)C, 256);
     L->bseq = take((size_t)c.B * 16, 256);
+    L->work = take(8, 64);
     L->seq_plan = take(8, 256);
     L->seq_base = take((size_t)C * 4, 256);
     L->seq_pop = take((size_t)C * 4, 256);
@@ -149,8 +150,7 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t
                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-int encode_pool_map(CUtensorMap *m, void *pool, int D, int n_pages) {
-    if (D % 64 != 0) return fail(RKV_ERR_UNSUPPORTED, "bf16 pools need D a multiple of 64");
+int encode_map(CUtensorMap *m, const void *base, const cuuint64_t *dims, const cuuint64_t *strides, const cuuint32_t *box) {
     static EncodeTiledFn fn = nullptr;
     if (!fn) {
         void *p = nullptr;
@@ -160,6 +160,16 @@ int encode_pool_map(CUtensorMap *m, void *pool, int D, int n_pages) {
             return fail(RKV_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
         fn = reinterpret_cast<EncodeTiledFn>(p);
     }
+    const cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(RKV_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+    return RKV_OK;
+}
+
+int encode_pool_map(CUtensorMap *m, void *pool, int D, int n_pages) {
+    if (D % 64 != 0) return fail(RKV_ERR_UNSUPPORTED, "bf16 pools need D a multiple of 64");
     // the pool as a 3-D tensor (64 columns, n_pages*16 rows, D/64 halves) of
     // bf16: one box is a whole page and lands in shared memory as D/64 planes
     // of 16 rows x 128 bytes, 16-byte chunks XOR-swizzled by line mod 8
@@ -167,12 +177,16 @@ int encode_pool_map(CUtensorMap *m, void *pool, int D, int n_pages) {
     const cuuint64_t dims[3] = {64, (cuuint64_t)n_pages * PAGE, nhalf};
     const cuuint64_t strides[2] = {(cuuint64_t)D * 2, 128};
     const cuuint32_t box[3] = {64, PAGE, nhalf};
-    const cuuint32_t estr[3] = {1, 1, 1};
-    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, pool, dims, strides, box, estr,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) return fail(RKV_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
-    return RKV_OK;
+    return encode_map(m, pool, dims, strides, box);
+}
+
+// Packed rows [n][heads][D] with `stride` elements between tokens, as (64
+// columns, n rows, heads*D/64 groups): one box is `rows` tokens of one head.
+int encode_rows_map(CUtensorMap *m, const void *base, int n, int heads, int D, int64_t stride, int rows) {
+    const cuuint64_t dims[3] = {64, (cuuint64_t)n, (cuuint64_t)heads * (D / 64)};
+    const cuuint64_t strides[2] = {(cuuint64_t)stride * 2, 128};
+    const cuuint32_t box[3] = {64, (cuuint32_t)rows, (cuuint32_t)(D / 64)};
+    return encode_map(m, base, dims, strides, box);
 }
 
 // Packed sequences: offsets cu[B+1] into n rows.
@@ -841,7 +855,19 @@ RKV_API int rkv_prompt_attn(const rkv_cache_t *cache, const int32_t *cu, int32_t
     a.Hq = cache->Hq;
     a.n_tokens = n_tokens;
     a.qscale = scale * 1.4426950408889634f;
-    cudaError_t e = launch_prompt(a, cache->dtype, cache->D, static_cast<cudaStream_t>(stream));
+    a.next = at<uint32_t>(ws, L.work);
+    cudaError_t e;
+    if (cache->dtype == RKV_BF16) {
+        CUtensorMap tq{}, tk{}, tv{};
+        if ((rc = encode_rows_map(&tq, q, n_tokens, cache->Hq, cache->D, q_stride, 128))) return rc;
+        if ((rc = encode_rows_map(&tk, k, n_tokens, cache->H, cache->D, k_stride, 128))) return rc;
+        if ((rc = encode_rows_map(&tv, v, n_tokens, cache->H, cache->D, v_stride, 128))) return rc;
+        int sms = 0;
+        if ((rc = sm_count_now(&sms))) return rc;
+        e = launch_prompt_tc(a, cache->D, sms, tq, tk, tv, static_cast<cudaStream_t>(stream));
+    } else {
+        e = launch_prompt(a, cache->D, static_cast<cudaStream_t>(stream));
+    }
     if (e != cudaSuccess) return cuda_fail(e, "rkv_prompt_attn");
     return RKV_OK;
 }

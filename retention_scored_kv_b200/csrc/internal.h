@@ -46,6 +46,7 @@ struct WsLayout {
     size_t bfloor;        // int32  [C] oldest floor position (ContourKV)
     size_t bskip;         // uint8  [C] flat heads (ContourKV)
     size_t bseq;          // uint64 [B][2] forced entries, entries left to rank (ContourKV)
+    size_t work;          // uint32 [2] next piece of work and CTAs that have left (self-resetting)
     size_t seq_plan;      // int32 [2] outcome of a sequence plan: go, free pages after it
     size_t seq_base;      // int32 [C] lengths a sequence operator works from
     size_t seq_pop;       // int32 [C] stack index of the first page each head takes
@@ -317,10 +318,14 @@ struct PromptArgs {
     void *out;
     float *lse;                // [n_tokens][Hq], may be NULL
     int32_t *status;
+    uint32_t *next;            // [2] next piece of work, CTAs that have left (self-resetting)
     int B, H, Hq, n_tokens;
     float qscale;              // scale * log2(e)
 };
-cudaError_t launch_prompt(const PromptArgs &a, int dtype, int D, cudaStream_t s);
+// fp32 (prompt.cu), and bf16 through tensor maps of 128-row tiles (prompt_tc.cu).
+cudaError_t launch_prompt(const PromptArgs &a, int D, cudaStream_t s);
+cudaError_t launch_prompt_tc(const PromptArgs &a, int D, int sms, const CUtensorMap &tq, const CUtensorMap &tk,
+                             const CUtensorMap &tv, cudaStream_t s);
 
 // Tree attention (tree.cu).
 constexpr int TREE_MAX_NODES = 64;  // a node's mask is one 64-bit word

@@ -1,5 +1,6 @@
 // prompt.cu -- rkv_prompt_attn: causal grouped-query attention over the
-// packed prompts of a batch (one layer a call).
+// packed prompts of a batch (one layer a call), on fp32 tensors; bf16 ones take
+// prompt_tc.cu.
 //
 //   o[i] = sum_{j <= i} exp(z_ij - lse_i) v_j,  z_ij = scale <q_i, k_j>,
 //   lse_i = log sum_{j <= i} exp(z_ij)
@@ -10,7 +11,7 @@ namespace rkv {
 namespace {
 
 // One CTA per (64 query rows, query head): FFMA products, see serve.cuh.
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(FT_THREADS) prompt_ffma_kernel(const PromptArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];
     FTile<D> &t = *reinterpret_cast<FTile<D> *>(smem);
@@ -28,9 +29,9 @@ __global__ void __launch_bounds__(FT_THREADS) prompt_ffma_kernel(const PromptArg
     if (w.b < 0) return;
     const int64_t t0 = s_cu[w.b];
     const int n = s_cu[w.b + 1] - s_cu[w.b], r0 = w.blk * FT_ROWS, h = hq / (a.Hq / a.H);
-    const T *q = static_cast<const T *>(a.q) + (int64_t)hq * D;
-    const T *k = static_cast<const T *>(a.k) + (int64_t)h * D;
-    const T *v = static_cast<const T *>(a.v) + (int64_t)h * D;
+    const float *q = static_cast<const float *>(a.q) + (int64_t)hq * D;
+    const float *k = static_cast<const float *>(a.k) + (int64_t)h * D;
+    const float *v = static_cast<const float *>(a.v) + (int64_t)h * D;
     constexpr int V4 = D / 4;
     for (int i = threadIdx.x; i < FT_ROWS * V4; i += FT_THREADS) {
         const int r = i / V4, d = i % V4 * 4;
@@ -63,7 +64,7 @@ __global__ void __launch_bounds__(FT_THREADS) prompt_ffma_kernel(const PromptArg
     for (int i = 0; i < 4; i++) {
         const int r = r0 + ty * 4 + i;
         if (r >= n) continue;
-        T *o = static_cast<T *>(a.out) + (t0 + r) * a.out_stride + (int64_t)hq * D;
+        float *o = static_cast<float *>(a.out) + (t0 + r) * a.out_stride + (int64_t)hq * D;
         const float inv = 1.f / st.l[i];
 #pragma unroll
         for (int j = 0; j < D / 64; j++)
@@ -73,23 +74,22 @@ __global__ void __launch_bounds__(FT_THREADS) prompt_ffma_kernel(const PromptArg
     }
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t launch_ffma(const PromptArgs &a, cudaStream_t s) {
     const size_t smem = sizeof(FTile<D>) + (size_t)(a.B + 1) * 4;
-    cudaError_t e = cudaFuncSetAttribute(prompt_ffma_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(prompt_ffma_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)smem);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (int64_t)(a.n_tokens / FT_ROWS + a.B) * a.Hq;
     if (tiles >= (1ll << 31)) return cudaErrorNotSupported;
-    prompt_ffma_kernel<T, D><<<(unsigned)tiles, FT_THREADS, smem, s>>>(a);
+    prompt_ffma_kernel<D><<<(unsigned)tiles, FT_THREADS, smem, s>>>(a);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_prompt(const PromptArgs &a, int dtype, int D, cudaStream_t s) {
-    if (dtype == RKV_BF16) return D == 64 ? launch_ffma<__nv_bfloat16, 64>(a, s) : launch_ffma<__nv_bfloat16, 128>(a, s);
-    return D == 64 ? launch_ffma<float, 64>(a, s) : launch_ffma<float, 128>(a, s);
+cudaError_t launch_prompt(const PromptArgs &a, int D, cudaStream_t s) {
+    return D == 64 ? launch_ffma<64>(a, s) : launch_ffma<128>(a, s);
 }
 
 }  // namespace rkv

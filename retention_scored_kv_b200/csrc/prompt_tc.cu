@@ -1,0 +1,508 @@
+// prompt_tc.cu -- rkv_prompt_attn on bf16: both products on the fifth-
+// generation tensor cores, accumulators in tensor memory.
+//
+// A CTA works on 256 query rows of one query head: two tiles of 128 rows (one
+// tensor-memory lane a row) against the same key tiles of 128.  Per key tile
+//   S_i = Q_i K^T        (128 x 128, tensor memory)
+//   P_i = exp(S_i - m_i) (warpgroup i: one thread a row, bf16 over S's columns)
+//   O_i += P_i V         (128 x D, tensor memory; P as the left operand)
+// While warpgroup 0 turns S_0 into P_0 the tensor core runs S_1, O_1 and back:
+// the exponentials of a tile (128 x 128 over 16 a cycle) take as long as its two
+// products, so the two have to overlap.  A row's output is rescaled only when
+// its maximum has grown by more than RESCALE (the weights then stay below
+// 2^RESCALE, far inside fp32 and bf16 range); each row's sum is of the unrounded
+// fp32 weights.
+//
+// Warps 0-3 and 4-7: softmax of tile 0 and 1, and the output.  Warp 8: TMA loads
+// through a ring of shared-memory slots, and the next piece of work.  Warp 9:
+// issues the products.  Warps 10, 11: V of the last two key tiles of a piece of
+// work, before the tensor core reads it: rows past the sequence's end become
+// zero and infinite or NaN values (which would reach rows that do not attend
+// them, as 0 * NaN) too; the output adds the latter for the rows that do.
+#include "internal.h"
+#include "serve.cuh"
+#include "tc5.cuh"
+
+namespace rkv {
+namespace {
+
+constexpr int QR = 128, KR = 128;   // rows of a query tile, of a key tile
+constexpr int THREADS = 384;
+constexpr float RESCALE = 8.f;
+
+template <int D>
+struct Cfg {
+    static constexpr int TILE = 128 * D * 2;               // bytes of a tile
+    static constexpr int SLOTS = D == 128 ? 5 : 8;         // K and V tiles in flight
+    static constexpr int SMEM = (2 + SLOTS) * TILE + 1024; // + alignment of the swizzle's period
+};
+
+struct Work {
+    int b, blk, hq, odd;  // odd: bit t: V of the t-th of the last two key tiles held infinities or NaN
+    int t0, n;            // first token and length of the sequence
+};
+
+struct Shared {
+    uint64_t full[8], empty[8];            // K / V slots
+    uint64_t q_full[2], q_empty[2];
+    uint64_t s_full[2], p_full[2], o_done[2], o_free[2];
+    uint64_t v_last[8], v_ready[8];        // a slot's V of the last key tiles: loaded, and mended (full is not used)
+    uint64_t w_full[2], w_empty[2];        // pieces of work
+    Work work[2];
+    uint32_t tmem;
+};
+
+// What a piece of work consists of: key tiles of each query tile.
+struct Shape {
+    int nk0, nk1, nk;
+    __device__ Shape(const Work &w) {
+        nk0 = 2 * w.blk + 1;
+        nk1 = (2 * w.blk + 1) * QR < w.n ? nk0 + 1 : 0;
+        nk = nk1 ? nk1 : nk0;
+    }
+};
+
+// Position in a ring of n slots and the parity of the wait for its use.
+struct Ring {
+    int slot = 0;
+    uint32_t turn = 0;
+    __device__ void next(int n) {
+        if (++slot == n) {
+            slot = 0;
+            turn ^= 1;
+        }
+    }
+};
+
+template <int D>
+struct Ctx {
+    Shared *sh;
+    unsigned char *q, *kv;
+    int32_t *status;
+    __device__ bool wait(uint64_t *bar, uint32_t parity, int site) const { return mbar_wait(bar, parity, status, site); }
+    __device__ unsigned char *slot(int i) const { return kv + (size_t)i * Cfg<D>::TILE; }
+};
+
+// ------------------------------------------------------------ warp 8: loads ----
+template <int D>
+__device__ void load_role(const Ctx<D> &x, const PromptArgs &a, const CUtensorMap *tq, const CUtensorMap *tk,
+                          const CUtensorMap *tv) {
+    using C = Cfg<D>;
+    const int lane = threadIdx.x & 31, G = a.Hq / a.H;
+    const int total = tiles_from(a.cu, a.B, 2 * QR, 0) * a.Hq;
+    Ring kv, w;
+    uint32_t q_turn[2] = {0, 0};
+    for (;; w.next(2)) {
+        int tile = 0;
+        if (lane == 0) tile = (int)atomicAdd(a.next, 1u);
+        tile = __shfl_sync(0xFFFFFFFFu, tile, 0);
+        const bool end = tile >= total;
+        SeqTile t{-1, 0};
+        if (!end) t = find_tile(a.cu, a.B, a.n_tokens, 2 * QR, tile / a.Hq);
+        int ok = 1;
+        if (lane == 0) {
+            ok = x.wait(&x.sh->w_empty[w.slot], w.turn ^ 1u, 0x400);
+            Work wk{t.b, t.blk, tile % a.Hq, 0, 0, 0};
+            if (!end) {
+                wk.t0 = a.cu[t.b];
+                wk.n = a.cu[t.b + 1] - wk.t0;
+            }
+            if (ok) {
+                x.sh->work[w.slot] = wk;
+                mbar_arrive(&x.sh->w_full[w.slot]);
+            }
+            if (ok && !end) {
+                const Shape s(wk);
+                const int h = wk.hq / G, planes = D / 64;
+                auto query = [&](int i) {
+                    if (!x.wait(&x.sh->q_empty[i], q_turn[i] ^ 1u, 0x401)) return false;
+                    q_turn[i] ^= 1u;
+                    mbar_arrive_expect_tx(&x.sh->q_full[i], C::TILE);
+                    tma_tile(x.q + i * C::TILE, tq, 0, wk.t0 + (2 * wk.blk + i) * QR, wk.hq * planes, &x.sh->q_full[i]);
+                    return true;
+                };
+                auto tile_of = [&](const CUtensorMap *m, int j) {
+                    if (!x.wait(&x.sh->empty[kv.slot], kv.turn ^ 1u, 0x402)) return false;
+                    uint64_t *bar = m == tv && j >= 2 * wk.blk ? &x.sh->v_last[kv.slot] : &x.sh->full[kv.slot];
+                    mbar_arrive_expect_tx(bar, C::TILE);
+                    tma_tile(x.slot(kv.slot), m, 0, wk.t0 + j * KR, h * planes, bar);
+                    kv.next(C::SLOTS);
+                    return true;
+                };
+                ok = query(0) && tile_of(tk, 0) && (!s.nk1 || query(1)) && tile_of(tv, 0);
+                for (int j = 1; ok && j < s.nk; j++) ok = tile_of(tk, j) && tile_of(tv, j);
+            }
+        }
+        ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+        if (!ok || end) return;
+    }
+}
+
+// ---------------------------------------------------------- warp 9: products ----
+template <int D>
+__device__ void mma_role(const Ctx<D> &x, bool neg) {
+    using C = Cfg<D>;
+    Shared *sh = x.sh;
+    const uint32_t tmem = sh->tmem;
+    const uint32_t qk = mma_desc(QR, KR, false, neg), pv = mma_desc(QR, D, true, false);
+    Ring kv, w;
+    uint32_t q_turn[2] = {0, 0}, p_turn[2] = {0, 0}, f_turn[2] = {0, 0};
+    uint32_t kv_turn = 0, v_turn = 0;  // full, v_ready: a bit for each slot
+    auto scores = [&](int i, int kslot) {
+        const uint32_t q0 = smem_u32(x.q + i * C::TILE), k0 = smem_u32(x.slot(kslot));
+#pragma unroll
+        for (int s = 0; s < D / 16; s++) {
+            const uint32_t off = (s / 4) * (128 * 128) + (s % 4) * 32;
+            mma_ss(tmem + i * 128, tile_desc(q0 + off, 16), tile_desc(k0 + off, 16), qk, s > 0);
+        }
+        mma_commit(&sh->s_full[i]);
+    };
+    auto output = [&](int i, int vslot, bool first) {
+        const uint32_t v0 = smem_u32(x.slot(vslot));
+#pragma unroll
+        for (int s = 0; s < KR / 16; s++)
+            mma_ts(tmem + 256 + i * D, tmem + i * 128 + s * 8, tile_desc(v0 + s * 2048, 128 * 128), pv, !first || s > 0);
+        mma_commit(&sh->o_done[i]);
+    };
+    for (;; w.next(2)) {
+        if (!x.wait(&sh->w_full[w.slot], w.turn, 0x410)) return;
+        const Work wk = sh->work[w.slot];
+        mbar_arrive(&sh->w_empty[w.slot]);
+        if (wk.b < 0) return;
+        const Shape s(wk);
+        int kslot = kv.slot;
+        if (!x.wait(&sh->full[kslot], kv_turn >> kslot & 1u, 0x411)) return;
+        kv_turn ^= 1u << kslot;
+        kv.next(C::SLOTS);
+        for (int i = 0; i < (s.nk1 ? 2 : 1); i++) {
+            if (!x.wait(&sh->q_full[i], q_turn[i], 0x412)) return;
+            q_turn[i] ^= 1u;
+            tc_fence_after();
+            scores(i, kslot);
+            if ((i ? s.nk1 : s.nk0) == 1) mma_commit(&sh->q_empty[i]);
+        }
+        mma_commit(&sh->empty[kslot]);
+        for (int j = 0; j < s.nk; j++) {
+            const int vslot = kv.slot;
+            if (j >= 2 * wk.blk) {
+                if (!x.wait(&sh->v_ready[vslot], v_turn >> vslot & 1u, 0x413)) return;
+                v_turn ^= 1u << vslot;
+            } else {
+                if (!x.wait(&sh->full[vslot], kv_turn >> vslot & 1u, 0x414)) return;
+                kv_turn ^= 1u << vslot;
+            }
+            kv.next(C::SLOTS);
+            kslot = kv.slot;
+            bool k_here = false;
+#pragma unroll 1
+            for (int i = 0; i < 2; i++) {
+                const int nk = i ? s.nk1 : s.nk0;
+                if (j >= nk) continue;
+                if (j == 0) {
+                    if (!x.wait(&sh->o_free[i], f_turn[i] ^ 1u, 0x415)) return;
+                    f_turn[i] ^= 1u;
+                }
+                if (!x.wait(&sh->p_full[i], p_turn[i], 0x416)) return;
+                p_turn[i] ^= 1u;
+                tc_fence_after();
+                output(i, vslot, j == 0);
+                if (j + 1 < nk) {
+                    if (!k_here) {
+                        if (!x.wait(&sh->full[kslot], kv_turn >> kslot & 1u, 0x417)) return;
+                        kv_turn ^= 1u << kslot;
+                        k_here = true;
+                    }
+                    scores(i, kslot);
+                    if (j + 2 == nk) mma_commit(&sh->q_empty[i]);
+                }
+            }
+            mma_commit(&sh->empty[vslot]);
+            if (j + 1 < s.nk) {
+                mma_commit(&sh->empty[kslot]);
+                kv.next(C::SLOTS);
+            }
+        }
+    }
+}
+
+// ------------------------------------------------- warps 10, 11: V's last tiles ----
+template <int D>
+__device__ void mend_role(const Ctx<D> &x) {
+    using C = Cfg<D>;
+    Shared *sh = x.sh;
+    const int t = threadIdx.x - 320;
+    Ring kv, w;
+    uint32_t turn = 0;  // v_last: a bit for each slot
+    for (;; w.next(2)) {
+        if (!x.wait(&sh->w_full[w.slot], w.turn, 0x420)) return;
+        const Work wk = sh->work[w.slot];
+        if (wk.b >= 0) {
+            const Shape s(wk);
+            for (int j = 0; j < s.nk; j++) {
+                kv.next(C::SLOTS);  // K
+                if (j >= 2 * wk.blk) {
+                    if (!x.wait(&sh->v_last[kv.slot], turn >> kv.slot & 1u, 0x421)) return;
+                    turn ^= 1u << kv.slot;
+                    const int rows = wk.n - j * KR;  // rows of the sequence from here on
+                    uint4 *tile = reinterpret_cast<uint4 *>(x.slot(kv.slot));
+                    uint32_t odd = 0;
+                    for (int i = t; i < C::TILE / 16; i += 64) {
+                        const int row = (i >> 3) & 127;
+                        uint4 v = make_uint4(0, 0, 0, 0);
+                        if (row < rows) {
+                            v = tile[i];
+                            uint32_t bad = 0;
+                            uint32_t *p = reinterpret_cast<uint32_t *>(&v);
+#pragma unroll
+                            for (int e = 0; e < 4; e++) {
+                                const uint32_t m = __vcmpeq2(p[e] & 0x7F807F80u, 0x7F807F80u);
+                                bad |= m;
+                                p[e] &= ~m;
+                            }
+                            if (!bad) continue;
+                            odd = 1;
+                        }
+                        tile[i] = v;
+                    }
+                    if (odd) atomicOr(&sh->work[w.slot].odd, 1 << (j - 2 * wk.blk));
+                    fence_async_shared();
+                    __syncwarp();
+                    if ((threadIdx.x & 31) == 0) mbar_arrive(&sh->v_ready[kv.slot]);
+                }
+                kv.next(C::SLOTS);  // V
+            }
+        }
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(&sh->w_empty[w.slot]);
+        if (wk.b < 0) return;
+    }
+}
+
+// ------------------------------------------------------ warps 0-7: softmax ----
+// S of one key tile to P: m is the row's reference maximum (of the raw scores),
+// l the sum of its weights so far.  Returns false on a wait that gave up.
+template <int D, bool DIAG>
+__device__ __forceinline__ bool softmax_tile(const Ctx<D> &x, int i, int j, uint32_t ts, uint32_t to, int row,
+                                             float qscale, float &m, float &l, uint32_t done_turn) {
+    uint32_t s[4][32];
+#pragma unroll
+    for (int c = 0; c < 4; c++) tmem_ld32(s[c], ts + c * 32);
+#pragma unroll
+    for (int c = 0; c < 4; c++) tmem_wait_ld32(s[c]);
+    if (DIAG) {
+#pragma unroll
+        for (int c = 0; c < 128; c++)
+            if (c > row) s[c / 32][c % 32] = 0xFF800000u;
+    }
+    float mx[4];
+#pragma unroll
+    for (int c = 0; c < 4; c++) {
+        mx[c] = __uint_as_float(s[c][0]);
+#pragma unroll
+        for (int e = 1; e < 32; e++) mx[c] = fmaxf(mx[c], __uint_as_float(s[c][e]));
+    }
+    const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+    const bool grow = (mt - m) * qscale > RESCALE || (j == 0);
+    if (__any_sync(0xFFFFFFFFu, grow)) {
+        // the whole warp moves to its new maxima (O is read and written by warps)
+        float mn = fmaxf(m, mt);
+        if (mn == -INFINITY) mn = 0.f;
+        if (j > 0) {
+            const float f = ex2((m - mn) * qscale);
+            l *= f;
+            if (!x.wait(&x.sh->o_done[i], done_turn, 0x430)) return false;
+            tc_fence_after();
+            for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                tmem_ld32(o, to + c);
+                tmem_wait_ld32(o);
+#pragma unroll
+                for (int e = 0; e < 32; e++) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st32(to + c, o);
+            }
+        }
+        m = mn;
+    }
+    const float2 qs = make_float2(qscale, qscale), mm = make_float2(-m * qscale, -m * qscale);
+    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+    for (int half = 0; half < 2; half++) {
+        uint32_t p[32];
+#pragma unroll
+        for (int e = 0; e < 32; e++) {
+            const int c = half * 64 + 2 * e;
+            float2 z = ffma2(make_float2(__uint_as_float(s[c / 32][c % 32]), __uint_as_float(s[c / 32][c % 32 + 1])), qs, mm);
+            z.x = ex2(z.x);
+            z.y = ex2(z.y);
+            sum[e & 1] = fadd2(sum[e & 1], z);
+            p[e] = pack_bf16(z.x, z.y);
+        }
+        tmem_st32(ts + half * 32, p);
+    }
+    sum[0] = fadd2(sum[0], sum[1]);
+    l += sum[0].x + sum[0].y;
+    tmem_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&x.sh->p_full[i]);
+    return true;
+}
+
+// Infinite and NaN values of V that the tensor core was not shown: add those
+// of the keys that this row attends.  Rare, and slow.
+__device__ __noinline__ void add_odd(float *o, const __nv_bfloat16 *v, int64_t stride, int first, int last) {
+    for (int j = first; j <= last; j++)
+        for (int e = 0; e < 32; e++) {
+            const float f = __bfloat162float(v[j * stride + e]);
+            if (!(fabsf(f) < INFINITY)) o[e] += f;
+        }
+}
+
+template <int D>
+__device__ void softmax_role(const Ctx<D> &x, const PromptArgs &a) {
+    Shared *sh = x.sh;
+    const int i = threadIdx.x >> 7, row = threadIdx.x & 127, lane = threadIdx.x & 31;
+    const uint32_t lanes = (uint32_t)(row & 96) << 16;
+    const uint32_t ts = sh->tmem + i * 128 + lanes, to = sh->tmem + 256 + i * D + lanes;
+    const float qscale = fabsf(a.qscale);
+    uint32_t s_turn = 0, d_turn = 0;  // d_turn: parity of the next product to complete
+    Ring w;
+    for (;; w.next(2)) {
+        if (!x.wait(&sh->w_full[w.slot], w.turn, 0x431)) return;
+        const Work wk = sh->work[w.slot];
+        if (wk.b < 0) return;
+        const Shape sp(wk);
+        const int nk = i ? sp.nk1 : sp.nk0;
+        if (nk) {
+            float m = -INFINITY, l = 0.f;
+            for (int j = 0; j < nk; j++) {
+                if (!x.wait(&sh->s_full[i], s_turn, 0x432)) return;
+                s_turn ^= 1u;
+                tc_fence_after();
+                // the product of tile j - 1 has parity d_turn ^ 1 once tile j's is awaited
+                const bool ok = j + 1 == nk ? softmax_tile<D, true>(x, i, j, ts, to, row, qscale, m, l, d_turn ^ 1u)
+                                            : softmax_tile<D, false>(x, i, j, ts, to, row, qscale, m, l, d_turn ^ 1u);
+                if (!ok) return;
+                d_turn ^= 1u;
+            }
+            if (!x.wait(&sh->o_done[i], d_turn ^ 1u, 0x433)) return;
+            tc_fence_after();
+            const int r = (2 * wk.blk + i) * QR + row;  // row of the sequence
+            const int odd = *(volatile int *)&sh->work[w.slot].odd;
+            const bool here = r < wk.n;
+            const float inv = 1.f / l;
+            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + (wk.t0 + (int64_t)r) * a.out_stride + (int64_t)wk.hq * D;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                tmem_ld32(o, to + c);
+                tmem_wait_ld32(o);
+                float f[32];
+#pragma unroll
+                for (int e = 0; e < 32; e++) f[e] = __uint_as_float(o[e]) * inv;
+                if (odd && here) {
+                    const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.v) + (int64_t)wk.t0 * a.v_stride +
+                                             (int64_t)(wk.hq / (a.Hq / a.H)) * D + c;
+                    add_odd(f, v, a.v_stride, 2 * wk.blk * KR, r);
+                }
+                if (here) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8)
+                        *reinterpret_cast<uint4 *>(out + c + e) =
+                            make_uint4(pack_bf16(f[e], f[e + 1]), pack_bf16(f[e + 2], f[e + 3]), pack_bf16(f[e + 4], f[e + 5]),
+                                       pack_bf16(f[e + 6], f[e + 7]));
+                }
+            }
+            tc_fence_before();
+            if (here && a.lse) a.lse[(wk.t0 + (int64_t)r) * a.Hq + wk.hq] = (m * qscale + log2f(l)) * LN2;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh->o_free[i]);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->w_empty[w.slot]);
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(THREADS, 1) prompt_tc_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tq,
+                                                               const __grid_constant__ CUtensorMap tk,
+                                                               const __grid_constant__ CUtensorMap tv) {
+    extern __shared__ unsigned char raw[];
+    __shared__ Shared sh;
+    unsigned char *tiles = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    const int warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < 8; s++) {
+            mbar_init(&sh.full[s], 1);
+            mbar_init(&sh.empty[s], 1);
+            mbar_init(&sh.v_last[s], 1);
+            mbar_init(&sh.v_ready[s], 2);
+        }
+        for (int i = 0; i < 2; i++) {
+            mbar_init(&sh.q_full[i], 1);
+            mbar_init(&sh.q_empty[i], 1);
+            mbar_init(&sh.s_full[i], 1);
+            mbar_init(&sh.p_full[i], 4);
+            mbar_init(&sh.o_done[i], 1);
+            mbar_init(&sh.o_free[i], 4);
+            mbar_init(&sh.w_full[i], 1);
+            mbar_init(&sh.w_empty[i], 11);  // products, eight softmax warps, two mending warps
+        }
+        fence_mbar_init();
+    }
+    if (warp == 9) tmem_alloc(&sh.tmem, 512);
+    const bool ok = load_offsets(a.cu, a.B, a.n_tokens, a.n_tokens, nullptr, a.status);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const Ctx<D> x{&sh, tiles, tiles + 2 * Cfg<D>::TILE, a.status};
+    // 384 threads x 168 registers at launch: 256 x 208 + 128 x 80 is no more
+    if (ok) {
+        if (warp < 8) {
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+            softmax_role<D>(x, a);
+        } else {
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+            if (warp == 8) load_role<D>(x, a, &tq, &tk, &tv);
+            else if (warp == 9) {
+                if ((threadIdx.x & 31) == 0) mma_role<D>(x, a.qscale < 0.f);
+            } else {
+                mend_role<D>(x);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(sh.tmem, 512);
+    }
+    // the last CTA to leave puts the counters back
+    if (threadIdx.x == 0) {
+        __threadfence();
+        if (atomicAdd(a.next + 1, 1u) == gridDim.x - 1) {
+            a.next[0] = 0u;
+            a.next[1] = 0u;
+        }
+    }
+}
+
+template <int D>
+cudaError_t launch(const PromptArgs &a, int sms, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                   cudaStream_t s) {
+    cudaError_t e = cudaFuncSetAttribute(prompt_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM);
+    if (e != cudaSuccess) return e;
+    const int64_t tiles = (int64_t)(a.n_tokens / (2 * QR) + a.B) * a.Hq;  // upper bound
+    prompt_tc_kernel<D><<<(unsigned)(tiles < sms ? tiles : sms), THREADS, Cfg<D>::SMEM, s>>>(a, tq, tk, tv);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_prompt_tc(const PromptArgs &a, int D, int sms, const CUtensorMap &tq, const CUtensorMap &tk,
+                             const CUtensorMap &tv, cudaStream_t s) {
+    return D == 64 ? launch<64>(a, sms, tq, tk, tv, s) : launch<128>(a, sms, tq, tk, tv, s);
+}
+
+}  // namespace rkv

@@ -12,7 +12,7 @@ namespace rkv {
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
 // ------------------------------------------------------ packed sequences ----
-// Copies the offsets cu[0..B] to shared memory and checks them: non-negative,
+// Copies the offsets cu[0..B] to shared memory (unless NULL) and checks them: non-negative,
 // non-decreasing, cu[B] <= n_tokens and no sequence longer than `longest`.
 // Every thread of the block calls it; false (and RKV_DEV_BAD_INPUT) means that
 // the whole call computes nothing.
@@ -21,7 +21,7 @@ __device__ __forceinline__ bool load_offsets(const int32_t *cu, int B, int n_tok
     int bad = 0;
     for (int i = threadIdx.x; i <= B; i += blockDim.x) {
         const int32_t v = __ldg(cu + i);
-        s_cu[i] = v;
+        if (s_cu) s_cu[i] = v;
         if (v < 0 || v > n_tokens) bad = 1;
         if (i > 0) {
             const int32_t u = __ldg(cu + i - 1);
@@ -39,10 +39,10 @@ struct SeqTile {
 };
 
 // Query tiles with block index >= m over all sequences.
-__device__ __forceinline__ int tiles_from(const int32_t *s_cu, int B, int rows, int m) {
+__device__ __forceinline__ int tiles_from(const int32_t *cu, int B, int rows, int m) {
     int n = 0;
     for (int b = threadIdx.x & 31; b < B; b += 32) {
-        const int nb = (s_cu[b + 1] - s_cu[b] + rows - 1) / rows;
+        const int nb = (cu[b + 1] - cu[b] + rows - 1) / rows;
         n += nb > m ? nb - m : 0;
     }
     return __reduce_add_sync(0xFFFFFFFFu, n);
@@ -53,18 +53,18 @@ __device__ __forceinline__ int tiles_from(const int32_t *s_cu, int B, int rows, 
 // tiles start first and the short ones fill the tail).  A whole warp calls it;
 // r must be below tiles_from(.., 0).  Bisection for the block index, then the
 // i-th sequence that has such a block: no list of tiles is stored.
-__device__ __forceinline__ SeqTile find_tile(const int32_t *s_cu, int B, int n_tokens, int rows, int r) {
+__device__ __forceinline__ SeqTile find_tile(const int32_t *cu, int B, int n_tokens, int rows, int r) {
     int lo = 0, hi = (n_tokens + rows - 1) / rows;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (tiles_from(s_cu, B, rows, mid) > r) lo = mid;
+        if (tiles_from(cu, B, rows, mid) > r) lo = mid;
         else hi = mid;
     }
-    int i = r - tiles_from(s_cu, B, rows, lo + 1);
+    int i = r - tiles_from(cu, B, rows, lo + 1);
     SeqTile t{0, lo};
     for (int b0 = 0; b0 < B; b0 += 32) {
         const int b = b0 + (threadIdx.x & 31);
-        const bool has = b < B && (s_cu[b + 1] - s_cu[b] + rows - 1) / rows > lo;
+        const bool has = b < B && (cu[b + 1] - cu[b] + rows - 1) / rows > lo;
         const uint32_t m = __ballot_sync(0xFFFFFFFFu, has);
         const int n = __popc(m);
         if (i < n) {
