@@ -181,13 +181,18 @@ int encode_pool_map(CUtensorMap *m, void *pool, int D, int n_pages) {
 }
 
 // Packed rows [n][heads][D] with `stride` elements between tokens, as (64
-// columns, n rows, heads*D/64 groups): one box is `rows` tokens of one head.
-int encode_rows_map(CUtensorMap *m, const void *base, int n, int heads, int D, int64_t stride, int rows) {
+// columns, n rows, heads*D/64 groups): one box is `rows` rows of `groups` groups
+// (a whole head: D/64).
+int encode_rows_map(CUtensorMap *m, const void *base, int n, int heads, int D, int64_t stride, int rows, int groups) {
     const cuuint64_t dims[3] = {64, (cuuint64_t)n, (cuuint64_t)heads * (D / 64)};
     const cuuint64_t strides[2] = {(cuuint64_t)stride * 2, 128};
-    const cuuint32_t box[3] = {64, (cuuint32_t)rows, (cuuint32_t)(D / 64)};
+    const cuuint32_t box[3] = {64, (cuuint32_t)rows, (cuuint32_t)groups};
     return encode_map(m, base, dims, strides, box);
 }
+
+// scale * log2(e).  A scale of 0 (every weight the same) is taken as one that no
+// logit survives: 0 times a left-out pair's -inf would be NaN.
+float attn_scale(float scale) { return scale == 0.f ? 1e-30f : scale * 1.4426950408889634f; }
 
 // Packed sequences: offsets cu[B+1] into n rows.
 int check_packed(const char *what, const rkv_cache_t *c, const int32_t *cu, int32_t n) {
@@ -222,7 +227,7 @@ TreeLayout tree_offsets(const rkv_cache_t &c, int max_nodes, size_t *ticket, siz
     ws_layout(c, &L);
     const TreeLayout t = tree_layout(c.dtype, c.D, c.Hq / c.H, (int64_t)c.B * c.L * c.H, max_nodes);
     *ticket = L.total;
-    *rec = (*ticket + t.tickets * 4 + 255) / 256 * 256;
+    *rec = (*ticket + t.head_bytes + 255) / 256 * 256;
     *total = *rec + t.rec_floats * 4;
     return t;
 }
@@ -854,14 +859,14 @@ RKV_API int rkv_prompt_attn(const rkv_cache_t *cache, const int32_t *cu, int32_t
     a.H = cache->H;
     a.Hq = cache->Hq;
     a.n_tokens = n_tokens;
-    a.qscale = scale * 1.4426950408889634f;
+    a.qscale = attn_scale(scale);
     a.next = at<uint32_t>(ws, L.work);
     cudaError_t e;
     if (cache->dtype == RKV_BF16) {
         CUtensorMap tq{}, tk{}, tv{};
-        if ((rc = encode_rows_map(&tq, q, n_tokens, cache->Hq, cache->D, q_stride, 128))) return rc;
-        if ((rc = encode_rows_map(&tk, k, n_tokens, cache->H, cache->D, k_stride, 128))) return rc;
-        if ((rc = encode_rows_map(&tv, v, n_tokens, cache->H, cache->D, v_stride, 128))) return rc;
+        if ((rc = encode_rows_map(&tq, q, n_tokens, cache->Hq, cache->D, q_stride, 128, cache->D / 64))) return rc;
+        if ((rc = encode_rows_map(&tk, k, n_tokens, cache->H, cache->D, k_stride, 128, cache->D / 64))) return rc;
+        if ((rc = encode_rows_map(&tv, v, n_tokens, cache->H, cache->D, v_stride, 128, cache->D / 64))) return rc;
         int sms = 0;
         if ((rc = sm_count_now(&sms))) return rc;
         e = launch_prompt_tc(a, cache->D, sms, tq, tk, tv, static_cast<cudaStream_t>(stream));
@@ -923,6 +928,7 @@ RKV_API int rkv_tree_attn(const rkv_cache_t *cache, const int32_t *cu, int32_t n
     a.lse = lse;
     a.status = at<int32_t>(ws, L.status);
     a.ticket = at<uint32_t>(ws, ticket);
+    a.join = at<int4>(ws, ticket);
     a.rec = at<float>(ws, rec);
     a.B = cache->B;
     a.LH = cache->L * cache->H;
@@ -934,8 +940,25 @@ RKV_API int rkv_tree_attn(const rkv_cache_t *cache, const int32_t *cu, int32_t n
     a.max_nodes = max_nodes;
     a.row_tiles = tl.row_tiles;
     a.parts = tl.parts;
-    a.qscale = scale * 1.4426950408889634f;
-    cudaError_t e = launch_tree(a, cache->dtype, cache->D, static_cast<cudaStream_t>(stream));
+    a.nt = tl.nt;
+    a.rec_tiles = tl.rec_tiles;
+    a.qscale = attn_scale(scale);
+    cudaError_t e;
+    if (cache->dtype == RKV_BF16) {
+        const int D = cache->D, rows = cache->n_pages * PAGE;
+        CUtensorMap tq{}, tk{}, tv{}, dk{}, dv{};
+        const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a.LH * G, (cuuint64_t)n_tokens};
+        const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)a.LH * G * D * 2};
+        const cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)a.nt};
+        if ((rc = encode_map(&tq, q, dims, strides, box))) return rc;
+        if ((rc = encode_rows_map(&tk, cache->k_pool, rows, 1, D, D, PAGE, 1))) return rc;
+        if ((rc = encode_rows_map(&tv, cache->v_pool, rows, 1, D, D, PAGE, 1))) return rc;
+        if ((rc = encode_rows_map(&dk, k_draft, n_tokens, a.LH, D, (int64_t)a.LH * D, PAGE, 1))) return rc;
+        if ((rc = encode_rows_map(&dv, v_draft, n_tokens, a.LH, D, (int64_t)a.LH * D, PAGE, 1))) return rc;
+        e = launch_tree_tc(a, D, tq, tk, tv, dk, dv, static_cast<cudaStream_t>(stream));
+    } else {
+        e = launch_tree(a, cache->D, static_cast<cudaStream_t>(stream));
+    }
     if (e != cudaSuccess) return cuda_fail(e, "rkv_tree_attn");
     return RKV_OK;
 }

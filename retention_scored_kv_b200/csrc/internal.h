@@ -342,20 +342,28 @@ struct TreeArgs {
     void *out;                 // [n_tokens][L][Hq][D]
     float *lse;                // may be NULL
     int32_t *status;
-    uint32_t *ticket;          // self-resetting
+    uint32_t *ticket;          // fp32: self-resetting
+    int4 *join;                // bf16: [TREE_CTAS] items cut by the end of each CTA's range
     float *rec;
     int B, LH, G, C, max_pages, n_pages, n_tokens, max_nodes;
-    int row_tiles, parts;
+    int row_tiles, parts;      // fp32: tiles of 64 rows, parts of the keys
+    int nt, rec_tiles;         // bf16: tokens of a query tile, query tiles of a record
     float qscale;
 };
 // The workspace's part for trees of up to max_nodes tokens.
 struct TreeLayout {
-    int row_tiles, parts;
-    size_t tickets;            // uint32
+    int row_tiles, parts, nt, rec_tiles;
+    size_t head_bytes;         // tickets or join descriptions
     size_t rec_floats;
 };
+constexpr int TREE_CTAS = 148;
 TreeLayout tree_layout(int dtype, int D, int G, int64_t C, int max_nodes);
-cudaError_t launch_tree(const TreeArgs &a, int dtype, int D, cudaStream_t s);
+// fp32 (tree.cu), and bf16 (tree_tc.cu) through tensor maps of the queries (nt
+// tokens x G heads), the pools' pages and the drafted tokens' K and V in groups
+// of 16, 64 columns each.
+cudaError_t launch_tree(const TreeArgs &a, int D, cudaStream_t s);
+cudaError_t launch_tree_tc(const TreeArgs &a, int D, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                           const CUtensorMap &dk, const CUtensorMap &dv, cudaStream_t s);
 
 // Whole sequences (sequences.cu).
 struct AppendTokensArgs {

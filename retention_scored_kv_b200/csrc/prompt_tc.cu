@@ -8,10 +8,7 @@
 //   O_i += P_i V         (128 x D, tensor memory; P as the left operand)
 // While warpgroup 0 turns S_0 into P_0 the tensor core runs S_1, O_1 and back:
 // the exponentials of a tile (128 x 128 over 16 a cycle) take as long as its two
-// products, so the two have to overlap.  A row's output is rescaled only when
-// its maximum has grown by more than RESCALE (the weights then stay below
-// 2^RESCALE, far inside fp32 and bf16 range); each row's sum is of the unrounded
-// fp32 weights.
+// products, so the two have to overlap.
 //
 // Warps 0-3 and 4-7: softmax of tile 0 and 1, and the output.  Warp 8: TMA loads
 // through a ring of shared-memory slots, and the next piece of work.  Warp 9:
@@ -19,24 +16,19 @@
 // work, before the tensor core reads it: rows past the sequence's end become
 // zero and infinite or NaN values (which would reach rows that do not attend
 // them, as 0 * NaN) too; the output adds the latter for the rows that do.
-#include "internal.h"
-#include "serve.cuh"
-#include "tc5.cuh"
+#include "attn_tc.cuh"
 
 namespace rkv {
 namespace {
 
-constexpr int QR = 128, KR = 128;   // rows of a query tile, of a key tile
-constexpr int THREADS = 384;
-constexpr float RESCALE = 8.f;
-
 template <int D>
 struct Cfg {
-    static constexpr int TILE = 128 * D * 2;               // bytes of a tile
+    static constexpr int TILE = TcCfg<D>::TILE;
     static constexpr int SLOTS = D == 128 ? 5 : 8;         // K and V tiles in flight
-    static constexpr int SMEM = (2 + SLOTS) * TILE + 1024; // + alignment of the swizzle's period
+    static constexpr int SMEM = (2 + SLOTS) * TILE + 1024; // two query tiles; alignment of the swizzle's period
 };
 
+// A piece of work.
 struct Work {
     int b, blk, hq, odd;  // odd: bit t: V of the t-th of the last two key tiles held infinities or NaN
     int t0, n;            // first token and length of the sequence
@@ -59,18 +51,6 @@ struct Shape {
         nk0 = 2 * w.blk + 1;
         nk1 = (2 * w.blk + 1) * QR < w.n ? nk0 + 1 : 0;
         nk = nk1 ? nk1 : nk0;
-    }
-};
-
-// Position in a ring of n slots and the parity of the wait for its use.
-struct Ring {
-    int slot = 0;
-    uint32_t turn = 0;
-    __device__ void next(int n) {
-        if (++slot == n) {
-            slot = 0;
-            turn ^= 1;
-        }
     }
 };
 
@@ -149,19 +129,11 @@ __device__ void mma_role(const Ctx<D> &x, bool neg) {
     uint32_t q_turn[2] = {0, 0}, p_turn[2] = {0, 0}, f_turn[2] = {0, 0};
     uint32_t kv_turn = 0, v_turn = 0;  // full, v_ready: a bit for each slot
     auto scores = [&](int i, int kslot) {
-        const uint32_t q0 = smem_u32(x.q + i * C::TILE), k0 = smem_u32(x.slot(kslot));
-#pragma unroll
-        for (int s = 0; s < D / 16; s++) {
-            const uint32_t off = (s / 4) * (128 * 128) + (s % 4) * 32;
-            mma_ss(tmem + i * 128, tile_desc(q0 + off, 16), tile_desc(k0 + off, 16), qk, s > 0);
-        }
+        mma_scores<D>(tmem + TM_S + i * 128, x.q + i * C::TILE, x.slot(kslot), qk);
         mma_commit(&sh->s_full[i]);
     };
     auto output = [&](int i, int vslot, bool first) {
-        const uint32_t v0 = smem_u32(x.slot(vslot));
-#pragma unroll
-        for (int s = 0; s < KR / 16; s++)
-            mma_ts(tmem + 256 + i * D, tmem + i * 128 + s * 8, tile_desc(v0 + s * 2048, 128 * 128), pv, !first || s > 0);
+        mma_output<D>(tmem + TM_O + i * D, tmem + TM_S + i * 128, x.slot(vslot), pv, first);
         mma_commit(&sh->o_done[i]);
     };
     for (;; w.next(2)) {
@@ -251,15 +223,7 @@ __device__ void mend_role(const Ctx<D> &x) {
                         uint4 v = make_uint4(0, 0, 0, 0);
                         if (row < rows) {
                             v = tile[i];
-                            uint32_t bad = 0;
-                            uint32_t *p = reinterpret_cast<uint32_t *>(&v);
-#pragma unroll
-                            for (int e = 0; e < 4; e++) {
-                                const uint32_t m = __vcmpeq2(p[e] & 0x7F807F80u, 0x7F807F80u);
-                                bad |= m;
-                                p[e] &= ~m;
-                            }
-                            if (!bad) continue;
+                            if (!drop_odd(v)) continue;
                             odd = 1;
                         }
                         tile[i] = v;
@@ -279,91 +243,12 @@ __device__ void mend_role(const Ctx<D> &x) {
 }
 
 // ------------------------------------------------------ warps 0-7: softmax ----
-// S of one key tile to P: m is the row's reference maximum (of the raw scores),
-// l the sum of its weights so far.  Returns false on a wait that gave up.
-template <int D, bool DIAG>
-__device__ __forceinline__ bool softmax_tile(const Ctx<D> &x, int i, int j, uint32_t ts, uint32_t to, int row,
-                                             float qscale, float &m, float &l, uint32_t done_turn) {
-    uint32_t s[4][32];
-#pragma unroll
-    for (int c = 0; c < 4; c++) tmem_ld32(s[c], ts + c * 32);
-#pragma unroll
-    for (int c = 0; c < 4; c++) tmem_wait_ld32(s[c]);
-    if (DIAG) {
-#pragma unroll
-        for (int c = 0; c < 128; c++)
-            if (c > row) s[c / 32][c % 32] = 0xFF800000u;
-    }
-    float mx[4];
-#pragma unroll
-    for (int c = 0; c < 4; c++) {
-        mx[c] = __uint_as_float(s[c][0]);
-#pragma unroll
-        for (int e = 1; e < 32; e++) mx[c] = fmaxf(mx[c], __uint_as_float(s[c][e]));
-    }
-    const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-    const bool grow = (mt - m) * qscale > RESCALE || (j == 0);
-    if (__any_sync(0xFFFFFFFFu, grow)) {
-        // the whole warp moves to its new maxima (O is read and written by warps)
-        float mn = fmaxf(m, mt);
-        if (mn == -INFINITY) mn = 0.f;
-        if (j > 0) {
-            const float f = ex2((m - mn) * qscale);
-            l *= f;
-            if (!x.wait(&x.sh->o_done[i], done_turn, 0x430)) return false;
-            tc_fence_after();
-            for (int c = 0; c < D; c += 32) {
-                uint32_t o[32];
-                tmem_ld32(o, to + c);
-                tmem_wait_ld32(o);
-#pragma unroll
-                for (int e = 0; e < 32; e++) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                tmem_st32(to + c, o);
-            }
-        }
-        m = mn;
-    }
-    const float2 qs = make_float2(qscale, qscale), mm = make_float2(-m * qscale, -m * qscale);
-    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-    for (int half = 0; half < 2; half++) {
-        uint32_t p[32];
-#pragma unroll
-        for (int e = 0; e < 32; e++) {
-            const int c = half * 64 + 2 * e;
-            float2 z = ffma2(make_float2(__uint_as_float(s[c / 32][c % 32]), __uint_as_float(s[c / 32][c % 32 + 1])), qs, mm);
-            z.x = ex2(z.x);
-            z.y = ex2(z.y);
-            sum[e & 1] = fadd2(sum[e & 1], z);
-            p[e] = pack_bf16(z.x, z.y);
-        }
-        tmem_st32(ts + half * 32, p);
-    }
-    sum[0] = fadd2(sum[0], sum[1]);
-    l += sum[0].x + sum[0].y;
-    tmem_wait_st();
-    tc_fence_before();
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(&x.sh->p_full[i]);
-    return true;
-}
-
-// Infinite and NaN values of V that the tensor core was not shown: add those
-// of the keys that this row attends.  Rare, and slow.
-__device__ __noinline__ void add_odd(float *o, const __nv_bfloat16 *v, int64_t stride, int first, int last) {
-    for (int j = first; j <= last; j++)
-        for (int e = 0; e < 32; e++) {
-            const float f = __bfloat162float(v[j * stride + e]);
-            if (!(fabsf(f) < INFINITY)) o[e] += f;
-        }
-}
-
 template <int D>
 __device__ void softmax_role(const Ctx<D> &x, const PromptArgs &a) {
     Shared *sh = x.sh;
     const int i = threadIdx.x >> 7, row = threadIdx.x & 127, lane = threadIdx.x & 31;
     const uint32_t lanes = (uint32_t)(row & 96) << 16;
-    const uint32_t ts = sh->tmem + i * 128 + lanes, to = sh->tmem + 256 + i * D + lanes;
+    const uint32_t ts = sh->tmem + TM_S + i * 128 + lanes, to = sh->tmem + TM_O + i * D + lanes;
     const float qscale = fabsf(a.qscale);
     uint32_t s_turn = 0, d_turn = 0;  // d_turn: parity of the next product to complete
     Ring w;
@@ -380,8 +265,15 @@ __device__ void softmax_role(const Ctx<D> &x, const PromptArgs &a) {
                 s_turn ^= 1u;
                 tc_fence_after();
                 // the product of tile j - 1 has parity d_turn ^ 1 once tile j's is awaited
-                const bool ok = j + 1 == nk ? softmax_tile<D, true>(x, i, j, ts, to, row, qscale, m, l, d_turn ^ 1u)
-                                            : softmax_tile<D, false>(x, i, j, ts, to, row, qscale, m, l, d_turn ^ 1u);
+                auto done = [&] { return x.wait(&sh->o_done[i], d_turn ^ 1u, 0x430); };
+                auto causal = [&](uint32_t(&s)[4][32]) {
+#pragma unroll
+                    for (int c = 0; c < KR; c++)
+                        if (c > row) s[c / 32][c % 32] = 0xFF800000u;
+                };
+                const bool ok =
+                    j + 1 == nk ? softmax_tile<D>(ts, to, j == 0, qscale, m, l, &sh->p_full[i], causal, done)
+                                : softmax_tile<D>(ts, to, j == 0, qscale, m, l, &sh->p_full[i], [](auto &) {}, done);
                 if (!ok) return;
                 d_turn ^= 1u;
             }
@@ -403,15 +295,10 @@ __device__ void softmax_role(const Ctx<D> &x, const PromptArgs &a) {
                 if (odd && here) {
                     const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.v) + (int64_t)wk.t0 * a.v_stride +
                                              (int64_t)(wk.hq / (a.Hq / a.H)) * D + c;
-                    add_odd(f, v, a.v_stride, 2 * wk.blk * KR, r);
+                    for (int j = 2 * wk.blk * KR; j <= r; j++) add_odd(f, v + j * a.v_stride);
                 }
-                if (here) {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8)
-                        *reinterpret_cast<uint4 *>(out + c + e) =
-                            make_uint4(pack_bf16(f[e], f[e + 1]), pack_bf16(f[e + 2], f[e + 3]), pack_bf16(f[e + 4], f[e + 5]),
-                                       pack_bf16(f[e + 6], f[e + 7]));
-                }
+                if (here) store32(out + c, f);
+                __syncwarp();
             }
             tc_fence_before();
             if (here && a.lse) a.lse[(wk.t0 + (int64_t)r) * a.Hq + wk.hq] = (m * qscale + log2f(l)) * LN2;
@@ -424,7 +311,7 @@ __device__ void softmax_role(const Ctx<D> &x, const PromptArgs &a) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(THREADS, 1) prompt_tc_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tq,
+__global__ void __launch_bounds__(TC_THREADS, 1) prompt_tc_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tq,
                                                                const __grid_constant__ CUtensorMap tk,
                                                                const __grid_constant__ CUtensorMap tv) {
     extern __shared__ unsigned char raw[];
@@ -450,7 +337,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_tc_kernel(const PromptArgs 
         }
         fence_mbar_init();
     }
-    if (warp == 9) tmem_alloc(&sh.tmem, 512);
+    if (warp == 9) tmem_alloc(&sh.tmem, TM_COLS);
     const bool ok = load_offsets(a.cu, a.B, a.n_tokens, a.n_tokens, nullptr, a.status);
     tc_fence_before();
     __syncthreads();
@@ -476,7 +363,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_tc_kernel(const PromptArgs 
     if (warp == 9) {
         __syncwarp();
         tc_fence_after();
-        tmem_dealloc(sh.tmem, 512);
+        tmem_dealloc(sh.tmem, TM_COLS);
     }
     // the last CTA to leave puts the counters back
     if (threadIdx.x == 0) {
@@ -494,7 +381,7 @@ cudaError_t launch(const PromptArgs &a, int sms, const CUtensorMap &tq, const CU
     cudaError_t e = cudaFuncSetAttribute(prompt_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (int64_t)(a.n_tokens / (2 * QR) + a.B) * a.Hq;  // upper bound
-    prompt_tc_kernel<D><<<(unsigned)(tiles < sms ? tiles : sms), THREADS, Cfg<D>::SMEM, s>>>(a, tq, tk, tv);
+    prompt_tc_kernel<D><<<(unsigned)(tiles < sms ? tiles : sms), TC_THREADS, Cfg<D>::SMEM, s>>>(a, tq, tk, tv);
     return cudaGetLastError();
 }
 

@@ -3,8 +3,6 @@
 // the fp32 attention tile.
 #pragma once
 
-#include <cuda_bf16.h>
-
 #include "common.cuh"
 
 namespace rkv {
@@ -205,18 +203,7 @@ __device__ __forceinline__ bool odd4(float4 x) {
     return !(fabsf(x.x) < INFINITY && fabsf(x.y) < INFINITY && fabsf(x.z) < INFINITY && fabsf(x.w) < INFINITY);
 }
 
-// Four consecutive elements of a row as fp32.
 __device__ __forceinline__ float4 ld4(const float *p) { return __ldg(reinterpret_cast<const float4 *>(p)); }
-__device__ __forceinline__ float4 ld4(const __nv_bfloat16 *p) {
-    const uint2 w = __ldg(reinterpret_cast<const uint2 *>(p));
-    const float2 a = bf16x2_to_f2(w.x), b = bf16x2_to_f2(w.y);
-    return make_float4(a.x, a.y, b.x, b.y);
-}
 __device__ __forceinline__ void st4(float *p, float4 x) { *reinterpret_cast<float4 *>(p) = x; }
-__device__ __forceinline__ void st4(__nv_bfloat16 *p, float4 x) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), b = __floats2bfloat162_rn(x.z, x.w);
-    *reinterpret_cast<uint2 *>(p) = make_uint2(*reinterpret_cast<const uint32_t *>(&a),
-                                               *reinterpret_cast<const uint32_t *>(&b));
-}
 
 }  // namespace rkv

@@ -3,6 +3,7 @@
 // attends the head's kept cache entries and the drafted tokens j of its own
 // sequence with bit j of mask[i] set:
 //   o = sum_{kept cache} exp(z - lse) v + sum_{j in mask[i]} exp(z_j - lse) v_j
+// This file: fp32 pools; bf16 ones take tree_tc.cu.
 #include "internal.h"
 #include "serve.cuh"
 
@@ -17,7 +18,7 @@ constexpr int32_t KEY_CACHE = -1, KEY_NONE = -2;  // >= 0: drafted token
 // of either.  Parts of one (head, rows) meet through records in the workspace:
 // the last to arrive joins them in ascending order, so the result does not
 // depend on which one that is.
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(FT_THREADS) tree_ffma_kernel(const TreeArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];
     FTile<D> &t = *reinterpret_cast<FTile<D> *>(smem);
@@ -36,7 +37,7 @@ __global__ void __launch_bounds__(FT_THREADS) tree_ffma_kernel(const TreeArgs a)
     const int np = (m + PAGE - 1) / PAGE, tiles = (np + (nodes + PAGE - 1) / PAGE + 3) / 4;
     if (threadIdx.x < nodes) s_mask[threadIdx.x] = __ldg(a.mask + t0 + threadIdx.x);
     constexpr int V4 = D / 4;
-    const T *q = static_cast<const T *>(a.q);
+    const float *q = static_cast<const float *>(a.q);
     for (int i = threadIdx.x; i < FT_ROWS * V4; i += FT_THREADS) {
         const int r = r0 + i / V4, d = i % V4 * 4;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -52,7 +53,7 @@ __global__ void __launch_bounds__(FT_THREADS) tree_ffma_kernel(const TreeArgs a)
         if (threadIdx.x < FT_KEYS) {
             const int u = j0 * 4 + threadIdx.x / PAGE, off = threadIdx.x % PAGE;
             int32_t kind = KEY_NONE;
-            const T *kr = nullptr, *vr = nullptr;
+            const float *kr = nullptr, *vr = nullptr;
             if (u < np) {
                 const int32_t page = __ldg(a.block_table + (int64_t)c * a.max_pages + u);
                 const bool kept = !a.keep_mask || (__ldg(a.keep_mask + (int64_t)c * a.max_pages + u) >> off & 1);
@@ -60,15 +61,15 @@ __global__ void __launch_bounds__(FT_THREADS) tree_ffma_kernel(const TreeArgs a)
                     set_status(a.status, RKV_DEV_BAD_INPUT);
                 } else if (kept && u * PAGE + off < m) {
                     kind = KEY_CACHE;
-                    kr = static_cast<const T *>(a.k_pool) + ((int64_t)page * PAGE + off) * D;
-                    vr = static_cast<const T *>(a.v_pool) + ((int64_t)page * PAGE + off) * D;
+                    kr = static_cast<const float *>(a.k_pool) + ((int64_t)page * PAGE + off) * D;
+                    vr = static_cast<const float *>(a.v_pool) + ((int64_t)page * PAGE + off) * D;
                 }
             } else {
                 const int j = (u - np) * PAGE + off;
                 if (j < nodes) {
                     kind = j;
-                    kr = static_cast<const T *>(a.k_draft) + ((int64_t)(t0 + j) * a.LH + lh) * D;
-                    vr = static_cast<const T *>(a.v_draft) + ((int64_t)(t0 + j) * a.LH + lh) * D;
+                    kr = static_cast<const float *>(a.k_draft) + ((int64_t)(t0 + j) * a.LH + lh) * D;
+                    vr = static_cast<const float *>(a.v_draft) + ((int64_t)(t0 + j) * a.LH + lh) * D;
                 }
             }
             some = kind != KEY_CACHE;
@@ -82,8 +83,8 @@ __global__ void __launch_bounds__(FT_THREADS) tree_ffma_kernel(const TreeArgs a)
             const int r = i / V4, d = i % V4 * 4;
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
             if (s_k[r]) {
-                x = ld4(static_cast<const T *>(s_k[r]) + d);
-                y = ld4(static_cast<const T *>(s_v[r]) + d);
+                x = ld4(static_cast<const float *>(s_k[r]) + d);
+                y = ld4(static_cast<const float *>(s_v[r]) + d);
                 odd |= odd4(y);
             }
             *reinterpret_cast<float4 *>(&t.k[r][d]) = x;
@@ -147,7 +148,7 @@ __global__ void __launch_bounds__(FT_THREADS) tree_ffma_kernel(const TreeArgs a)
         const int r = r0 + ty * 4 + i;
         if (r >= R) continue;
         const int64_t at = (int64_t)(t0 + r / G) * a.LH * G + lh * G + r % G;
-        T *o = static_cast<T *>(a.out) + at * D;
+        float *o = static_cast<float *>(a.out) + at * D;
         const bool none = st.m[i] == -INFINITY && st.l[i] == 0.f;
         const float inv = none ? 0.f : 1.f / st.l[i];
 #pragma unroll
@@ -158,15 +159,15 @@ __global__ void __launch_bounds__(FT_THREADS) tree_ffma_kernel(const TreeArgs a)
     }
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t launch_ffma(const TreeArgs &a, cudaStream_t s) {
     const size_t smem = sizeof(FTile<D>) + (size_t)(a.B + 1) * 4;
-    cudaError_t e = cudaFuncSetAttribute(tree_ffma_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(tree_ffma_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)smem);
     if (e != cudaSuccess) return e;
     const int64_t ctas = (int64_t)a.C * a.row_tiles * a.parts;
     if (ctas >= (1ll << 31)) return cudaErrorNotSupported;
-    tree_ffma_kernel<T, D><<<(unsigned)ctas, FT_THREADS, smem, s>>>(a);
+    tree_ffma_kernel<D><<<(unsigned)ctas, FT_THREADS, smem, s>>>(a);
     return cudaGetLastError();
 }
 
@@ -180,21 +181,27 @@ static int ffma_parts(int64_t items) {
 }
 
 TreeLayout tree_layout(int dtype, int D, int G, int64_t C, int max_nodes) {
-    (void)dtype;
     TreeLayout L{};
+    if (dtype == RKV_BF16) {
+        L.nt = 128 / G < max_nodes ? 128 / G : max_nodes;
+        L.rec_tiles = max_nodes > L.nt ? 2 : 1;
+        L.head_bytes = TREE_CTAS * sizeof(int4);
+        // a CTA's range begins and ends inside an item at most: two records
+        L.rec_floats = (size_t)TREE_CTAS * 2 * L.rec_tiles * 128 * (D + 2);
+        return L;
+    }
     L.row_tiles = (max_nodes * G + FT_ROWS - 1) / FT_ROWS;
     const int64_t items = C * L.row_tiles;
     L.parts = ffma_parts(items);
-    // as many for every max_nodes: calls of different sizes share a workspace,
-    // and a record of one must not land on another's (zeroed) tickets
-    L.tickets = (size_t)C * ((TREE_MAX_NODES * G + FT_ROWS - 1) / FT_ROWS);
+    // as many tickets for every max_nodes: calls of different sizes share a
+    // workspace, and a record of one must not land on another's (zeroed) tickets
+    L.head_bytes = (size_t)C * ((TREE_MAX_NODES * G + FT_ROWS - 1) / FT_ROWS) * 4;
     L.rec_floats = L.parts > 1 ? (size_t)items * L.parts * FT_ROWS * (D + 2) : 0;
     return L;
 }
 
-cudaError_t launch_tree(const TreeArgs &a, int dtype, int D, cudaStream_t s) {
-    if (dtype == RKV_BF16) return D == 64 ? launch_ffma<__nv_bfloat16, 64>(a, s) : launch_ffma<__nv_bfloat16, 128>(a, s);
-    return D == 64 ? launch_ffma<float, 64>(a, s) : launch_ffma<float, 128>(a, s);
+cudaError_t launch_tree(const TreeArgs &a, int D, cudaStream_t s) {
+    return D == 64 ? launch_ffma<64>(a, s) : launch_ffma<128>(a, s);
 }
 
 }  // namespace rkv

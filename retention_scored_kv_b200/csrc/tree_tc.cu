@@ -1,0 +1,667 @@
+// tree_tc.cu -- rkv_tree_attn on bf16 pools: both products on the fifth-
+// generation tensor cores, K and V pages gathered by TMA.
+//
+// Per KV head the query rows are (drafted token, query head of the group), the
+// keys its cache pages and then its drafted tokens in groups of 16 rows; a key
+// tile is eight such groups.  An item is a head with at most two query tiles of
+// whole tokens (nt = 128 / G tokens each).  With two tiles both meet every key
+// tile, so K and V are read once for 256 rows; with one tile the two softmax
+// warpgroups take the key tiles in turn, each with its own running state, and
+// join at the end.
+//
+// All items' key tiles in order, plus COST per item for its queries and results,
+// are cut into one equal range per CTA: the work is bound by the bytes of K and
+// V, and heads differ in length by orders of magnitude.  An item cut by a range's
+// end leaves its parts' unnormalised outputs, maxima and sums in the workspace,
+// and tree_join_kernel joins them in ascending order.
+//
+// Warps 0-7: softmax and results.  Warp 8: pages, TMA loads, keep words.  Warp 9:
+// issues the products.  Warps 10, 11: V of key tiles with rows that do not
+// count: those become zero (0 * NaN would reach every row), and infinite or NaN
+// values of drafted tokens too (not every row attends them; the results add them
+// for those that do).
+#include "attn_tc.cuh"
+
+namespace rkv {
+namespace {
+
+constexpr int COST = 1;       // an item's queries and results, in key tiles
+constexpr int MIN_RANGE = 4;  // key tiles of a CTA at least: a cut costs a record and a join
+constexpr int WORDS = 8;      // ring of key tiles' keep words
+
+template <int D>
+struct Cfg {
+    static constexpr int TILE = TcCfg<D>::TILE, PLANE = TcCfg<D>::PLANE;
+    // K and V tiles in flight: 64 KB or more of each SM's share of HBM's latency
+    static constexpr int SLOTS = D == 128 ? 4 : 8;
+    static constexpr int SMEM = (2 + SLOTS) * TILE + 1024; // two query tiles; alignment of the swizzle's period
+};
+
+__host__ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+struct Item {
+    int c, t0, node0, nodes;  // head, first token of its sequence, first token of the item's, tokens of the sequence
+    int rows[2];              // rows of the query tiles (rows[1] = 0: one tile)
+    int lo, hi, np;           // key tiles of this part; cache pages of the head
+    int rec;                  // -1: the item is whole; else the record of this part
+    int odd;                  // V of some drafted token held infinities or NaN
+};
+
+struct __align__(16) Tile {
+    uint16_t word[8];  // bit r: row r of group g counts
+    uint32_t part;     // some row does not count, or a drafted token is among them
+    uint32_t pad[3];
+};
+
+struct Mend {
+    int slot, tile, item, draft;  // draft: bit g: group g is of drafted tokens
+};
+
+struct Shared {
+    uint64_t full[8], empty[8];     // K / V slots
+    uint64_t v_part[8], v_ready[8]; // a slot's V of a partial tile: loaded, and mended
+    uint64_t q_full[2], q_empty[2];
+    uint64_t s_full[2], p_full[2], o_done[2], o_free, ml_full;
+    uint64_t w_full[2], w_empty[2]; // items
+    uint64_t m_full[4], m_empty[4]; // tiles to mend
+    Item item[2];
+    Tile tile[WORDS];
+    Mend mend[4];
+    float2 ml[2][2][QR];            // one-tile items: maximum and sum of both warpgroups (by item, warpgroup)
+    uint32_t tmem;
+    int c0, p0;                     // first head of this CTA's range and the work before it
+    int begin, end, total;
+};
+
+template <int D>
+struct Ctx {
+    Shared *sh;
+    unsigned char *q, *kv;
+    int32_t *status;
+    __device__ bool wait(uint64_t *bar, uint32_t parity, int site) const { return mbar_wait(bar, parity, status, site); }
+    __device__ unsigned char *slot(int i) const { return kv + (size_t)i * Cfg<D>::TILE; }
+};
+
+// Key tiles of head c and items it is cut into.
+struct Head {
+    int t0, nodes, len, np, tiles, items;
+    __device__ Head(const TreeArgs &a, int c, int32_t *status) {
+        const int b = c / a.LH;
+        t0 = __ldg(a.cu + b);
+        nodes = __ldg(a.cu + b + 1) - t0;
+        len = clamp_len(__ldg(a.len + c), a.max_pages, status);
+        np = ceil_div(len, PAGE);
+        tiles = ceil_div(np + ceil_div(nodes, PAGE), 8);
+        items = nodes == 0 ? 0 : nodes <= a.nt ? 1 : ceil_div(nodes, 2 * a.nt);
+    }
+};
+
+// Start of CTA i's range when `total` is cut into n.
+__device__ __forceinline__ int cut(int total, int i, int n) { return (int)((int64_t)total * i / n); }
+// CTA whose range holds position x.
+__device__ __forceinline__ int cta_of(int total, int x, int n) {
+    int i = (int)((int64_t)x * n / total);
+    while (cut(total, i + 1, n) <= x) i++;
+    while (cut(total, i, n) > x) i--;
+    return i;
+}
+
+// ------------------------------------------------------------ warp 8: loads ----
+template <int D>
+__device__ void load_role(const Ctx<D> &x, const TreeArgs &a, int n, const CUtensorMap *tq, const CUtensorMap *tk,
+                          const CUtensorMap *tv, const CUtensorMap *dk, const CUtensorMap *dv) {
+    using C = Cfg<D>;
+    Shared *sh = x.sh;
+    const int lane = threadIdx.x & 31, cta = blockIdx.x;
+    Ring kv, w, qr, mr;
+    int tile_no = 0, pre = sh->p0;
+    bool ok = true;
+    auto wait = [&](uint64_t *bar, uint32_t parity, int site) {  // whole warp
+        int good = 1;
+        if (lane == 0) good = x.wait(bar, parity, site);
+        return __shfl_sync(0xFFFFFFFFu, good, 0) != 0;
+    };
+    for (int c = sh->c0; ok && c < a.C && pre < sh->end; c++) {
+        const Head h(a, c, a.status);
+        const int lh = c % a.LH;
+        for (int k = 0; ok && k < h.items; k++, pre += h.tiles + COST) {
+            Item it{};
+            it.lo = max(0, min(h.tiles, sh->begin - pre - COST));
+            it.hi = max(0, min(h.tiles, sh->end - pre - COST));
+            if (it.lo >= it.hi) continue;
+            it.c = c;
+            it.t0 = h.t0;
+            it.nodes = h.nodes;
+            it.np = h.np;
+            it.node0 = k * 2 * a.nt;
+            const int left = h.nodes - it.node0;
+            it.rows[0] = min(left, a.nt) * a.G;
+            it.rows[1] = left > a.nt ? min(left - a.nt, a.nt) * a.G : 0;
+            it.rec = -1;
+            if (it.lo > 0 || it.hi < h.tiles) it.rec = 2 * cta + (it.lo == 0 ? 1 : 0);
+            if (!(ok = wait(&sh->w_empty[w.slot], w.turn ^ 1u, 0x440))) break;
+            if (lane == 0) {
+                sh->item[w.slot] = it;
+                mbar_arrive(&sh->w_full[w.slot]);
+                if (it.rec >= 0 && it.lo == 0) {
+                    // this CTA has the first part: it describes the item to the join
+                    const int s = pre + COST;
+                    a.join[cta] = make_int4(c, it.node0, cta_of(sh->total, s + h.tiles - 1, n), 0);
+                }
+            }
+            // the item's one or two query tiles, behind its first key tile: their
+            // slots are free only when the products of the item before are done
+            auto queries = [&] {
+                for (int i = 0; i < (it.rows[1] ? 2 : 1); i++) {
+                    if (!wait(&sh->q_empty[qr.slot], qr.turn ^ 1u, 0x441)) return false;
+                    if (lane == 0) mbar_arrive_expect_tx(&sh->q_full[qr.slot], (uint32_t)(a.nt * a.G * D * 2));
+                    __syncwarp();
+                    if (lane < D / 64)
+                        tma_tile(x.q + qr.slot * C::TILE + lane * C::PLANE, tq, lane * 64, lh * a.G,
+                                 h.t0 + it.node0 + i * a.nt, &sh->q_full[qr.slot]);
+                    qr.next(2);
+                }
+                return true;
+            };
+            // pages and keep words of 32 groups at a time, one a lane, read a batch ahead
+            const int32_t *table = a.block_table + (int64_t)c * a.max_pages;
+            const uint16_t *keep = a.keep_mask ? a.keep_mask + (int64_t)c * a.max_pages : nullptr;
+            int32_t page = 0, next_page = 0;
+            uint32_t word = 0, next_word = 0;
+            auto fetch = [&](int u) {  // group u
+                next_page = -1;
+                next_word = 0;
+                if (u < h.np) {
+                    next_page = __ldg(table + u);
+                    next_word = keep ? __ldg(keep + u) : 0xFFFFu;
+                    const int in = h.len - u * PAGE;
+                    if (in < PAGE) next_word &= (1u << in) - 1u;
+                } else if (u - h.np < ceil_div(h.nodes, PAGE)) {
+                    const int in = h.nodes - (u - h.np) * PAGE;
+                    next_page = h.t0 + (u - h.np) * PAGE;  // a row of the draft
+                    next_word = in < PAGE ? (1u << in) - 1u : 0xFFFFu;
+                }
+            };
+            fetch(it.lo * 8 + lane);
+            for (int j = it.lo; ok && j < it.hi; j++, tile_no++) {
+                const int at = (j - it.lo) & 3;
+                if (at == 0) {
+                    page = next_page;
+                    word = next_word;
+                    const int u = j * 8 + lane;
+                    if (u < h.np && (uint32_t)page >= (uint32_t)a.n_pages) {
+                        if (word) set_status(a.status, RKV_DEV_BAD_INPUT);
+                        word = 0;
+                    }
+                    fetch(u + 32);
+                }
+                const int u = j * 8 + (lane & 7);  // lanes 0-7 (and their copies) have this tile's groups
+                const int32_t pg = __shfl_sync(0xFFFFFFFFu, page, at * 8 + (lane & 7));
+                const uint32_t wd = __shfl_sync(0xFFFFFFFFu, word, at * 8 + (lane & 7));
+                const bool draft = u >= h.np;
+                const uint32_t live = __ballot_sync(0xFFFFFFFFu, lane < 8 && wd != 0);
+                const uint32_t part = __ballot_sync(0xFFFFFFFFu, lane < 8 && (wd != 0xFFFFu || draft));
+                const uint32_t drafts = __ballot_sync(0xFFFFFFFFu, lane < 8 && wd != 0 && draft);
+                const uint32_t bytes = __popc(live) * PAGE * D * 2;
+                for (int kvi = 0; kvi < 2; kvi++) {
+                    if (!(ok = wait(&sh->empty[kv.slot], kv.turn ^ 1u, 0x442))) break;
+                    uint64_t *bar = kvi && part ? &sh->v_part[kv.slot] : &sh->full[kv.slot];
+                    if (kvi == 0) {
+                        Tile *t = &sh->tile[tile_no % WORDS];
+                        if (lane < 8) t->word[lane] = (uint16_t)wd;
+                        if (lane == 0) t->part = part;
+                    } else if (part) {
+                        if (!(ok = wait(&sh->m_empty[mr.slot], mr.turn ^ 1u, 0x443))) break;
+                        if (lane == 0) {
+                            sh->mend[mr.slot] = Mend{kv.slot, tile_no % WORDS, w.slot, (int)drafts};
+                            mbar_arrive(&sh->m_full[mr.slot]);
+                        }
+                        mr.next(4);
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+                    __syncwarp();
+                    if (lane < 8 && wd) {
+                        unsigned char *dst = x.slot(kv.slot) + lane * PAGE * 128;
+#pragma unroll
+                        for (int p = 0; p < D / 64; p++) {
+                            if (!draft) tma_tile(dst + p * C::PLANE, kvi ? tv : tk, 0, pg * PAGE, p, bar);
+                            else tma_tile(dst + p * C::PLANE, kvi ? dv : dk, 0, pg, lh * (D / 64) + p, bar);
+                        }
+                    }
+                    kv.next(C::SLOTS);
+                }
+                if (ok && j == it.lo) ok = queries();
+            }
+            w.next(2);
+        }
+    }
+    // the end: an item without rows, and a tile to mend without a slot
+    if (ok && wait(&sh->w_empty[w.slot], w.turn ^ 1u, 0x444) && lane == 0) {
+        sh->item[w.slot].rows[0] = 0;
+        mbar_arrive(&sh->w_full[w.slot]);
+    }
+    if (ok && wait(&sh->m_empty[mr.slot], mr.turn ^ 1u, 0x445) && lane == 0) {
+        sh->mend[mr.slot].slot = -1;
+        mbar_arrive(&sh->m_full[mr.slot]);
+    }
+}
+
+// ---------------------------------------------------------- warp 9: products ----
+template <int D>
+__device__ void mma_role(const Ctx<D> &x, bool neg) {
+    using C = Cfg<D>;
+    Shared *sh = x.sh;
+    const uint32_t tmem = sh->tmem, qk = mma_desc(QR, KR, false, neg), pv = mma_desc(QR, D, true, false);
+    Ring w, qr;
+    int kv = 0, tile_no = 0;                 // slots taken so far (mod SLOTS), key tiles so far
+    uint32_t kv_turn = 0, v_turn = 0, q_turn = 0;  // a bit for each slot
+    uint32_t p_turn = 0, f_turn = 0;         // p_full: a bit for each tile; o_free
+    for (;; w.next(2)) {
+        if (!x.wait(&sh->w_full[w.slot], w.turn, 0x450)) return;
+        const int rows0 = sh->item[w.slot].rows[0], rows1 = sh->item[w.slot].rows[1];
+        const int n = sh->item[w.slot].hi - sh->item[w.slot].lo;
+        mbar_arrive(&sh->w_empty[w.slot]);
+        if (rows0 == 0) return;
+        const bool two = rows1 > 0;
+        int qs[2];
+        for (int i = 0; i < (two ? 2 : 1); i++) {
+            if (!x.wait(&sh->q_full[qr.slot], q_turn >> qr.slot & 1u, 0x451)) return;
+            q_turn ^= 1u << qr.slot;
+            qs[i] = qr.slot;
+            qr.next(2);
+        }
+        if (!two) qs[1] = qs[0];
+        // scores of key tile j into S_i; with two query tiles both, before its slot is given back
+        auto scores = [&](int j, int i, bool wait_k, bool last) {
+            const int slot = (kv + 2 * j) % C::SLOTS;
+            if (wait_k) {
+                if (!x.wait(&sh->full[slot], kv_turn >> slot & 1u, 0x452)) return false;
+                kv_turn ^= 1u << slot;
+            }
+            tc_fence_after();
+            mma_scores<D>(tmem + TM_S + i * 128, x.q + qs[i] * C::TILE, x.slot(slot), qk);
+            mma_commit(&sh->s_full[i]);
+            if (last) mma_commit(&sh->empty[slot]);
+            if (j == n - 1) {
+                if (two) mma_commit(&sh->q_empty[qs[i]]);
+                else mma_commit(&sh->q_empty[qs[0]]);
+            }
+            return true;
+        };
+        if (two) {
+            if (!scores(0, 0, true, false) || !scores(0, 1, false, true)) return;
+        } else {
+            if (!scores(0, 0, true, true) || (n > 1 && !scores(1, 1, true, true))) return;
+        }
+        for (int j = 0; j < n; j++) {
+            const int slot = (kv + 2 * j + 1) % C::SLOTS;
+            const bool part = *(volatile uint32_t *)&sh->tile[(tile_no + j) % WORDS].part != 0;
+            if (part) {
+                if (!x.wait(&sh->v_ready[slot], v_turn >> slot & 1u, 0x453)) return;
+                v_turn ^= 1u << slot;
+            } else {
+                if (!x.wait(&sh->full[slot], kv_turn >> slot & 1u, 0x454)) return;
+                kv_turn ^= 1u << slot;
+            }
+            if (j == 0) {
+                if (!x.wait(&sh->o_free, f_turn ^ 1u, 0x455)) return;
+                f_turn ^= 1u;
+            }
+#pragma unroll 1
+            for (int q = 0; q < (two ? 2 : 1); q++) {
+                const int i = two ? q : j & 1;
+                if (!x.wait(&sh->p_full[i], p_turn >> i & 1u, 0x456)) return;
+                p_turn ^= 1u << i;
+                tc_fence_after();
+                mma_output<D>(tmem + TM_O + i * D, tmem + TM_S + i * 128, x.slot(slot), pv, two ? j == 0 : j < 2);
+                mma_commit(&sh->o_done[i]);
+                const int nj = two ? j + 1 : j + 2;
+                if (nj < n && !scores(nj, i, !two || q == 0, !two || q == 1)) return;
+            }
+            mma_commit(&sh->empty[slot]);
+        }
+        kv = (kv + 2 * n) % C::SLOTS;
+        tile_no += n;
+    }
+}
+
+// ------------------------------------------------ warps 10, 11: V's odd rows ----
+template <int D>
+__device__ void mend_role(const Ctx<D> &x) {
+    using C = Cfg<D>;
+    Shared *sh = x.sh;
+    const int t = threadIdx.x - 320;
+    Ring mr;
+    uint32_t turn = 0;  // v_part: a bit for each slot
+    for (;; mr.next(4)) {
+        if (!x.wait(&sh->m_full[mr.slot], mr.turn, 0x460)) return;
+        const Mend md = sh->mend[mr.slot];
+        if (md.slot < 0) return;
+        if (!x.wait(&sh->v_part[md.slot], turn >> md.slot & 1u, 0x461)) return;
+        turn ^= 1u << md.slot;
+        uint4 *tile = reinterpret_cast<uint4 *>(x.slot(md.slot));
+        uint32_t odd = 0;
+        // 8 consecutive threads: a line of 128 bytes
+        for (int i = t; i < C::TILE / 16; i += 64) {
+            const int row = (i >> 3) & 127, g = row >> 4;
+            if (!(sh->tile[md.tile].word[g] >> (row & 15) & 1)) {
+                tile[i] = make_uint4(0, 0, 0, 0);
+            } else if (md.draft >> g & 1) {
+                uint4 v = tile[i];
+                if (drop_odd(v)) {
+                    odd = 1;
+                    tile[i] = v;
+                }
+            }
+        }
+        if (odd) atomicOr(&sh->item[md.item].odd, 1);
+        fence_async_shared();
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) {
+            mbar_arrive(&sh->v_ready[md.slot]);
+            mbar_arrive(&sh->m_empty[mr.slot]);
+        }
+    }
+}
+
+// ------------------------------------------------------ warps 0-7: softmax ----
+template <int D>
+__device__ void softmax_role(const Ctx<D> &x, const TreeArgs &a) {
+    Shared *sh = x.sh;
+    const int i = threadIdx.x >> 7, row = threadIdx.x & 127, lane = threadIdx.x & 31;
+    const uint32_t lanes = (uint32_t)(row & 96) << 16;
+    const uint32_t ts = sh->tmem + TM_S + i * 128 + lanes, o0 = sh->tmem + TM_O + lanes, to = o0 + i * D;
+    const float qscale = fabsf(a.qscale);
+    uint32_t s_turn = 0, d_turn[2] = {0, 0}, x_turn = 0;  // d_turn: parity of the next product to complete
+    int tile_no = 0;
+    uint32_t flip = 0;
+    Ring w;
+    for (;; w.next(2)) {
+        if (!x.wait(&sh->w_full[w.slot], w.turn, 0x470)) return;
+        const Item it = sh->item[w.slot];
+        if (it.rows[0] == 0) return;
+        const bool two = it.rows[1] > 0;
+        const int n = it.hi - it.lo, rows = two ? it.rows[i] : it.rows[0];
+        const bool warp_here = (row & 96) < rows;  // some row of this warp counts
+        const int node = it.node0 + (two ? i * a.nt : 0) + row / a.G;
+        unsigned long long mask = 0;
+        if (row < rows) mask = __ldg(a.mask + it.t0 + node);
+        float m = -INFINITY, l = 0.f;
+        int mine = 0;
+        for (int j = two ? 0 : i; j < n; j += two ? 1 : 2, mine++) {
+            if (!x.wait(&sh->s_full[i], s_turn, 0x471)) return;
+            s_turn ^= 1u;
+            if (warp_here) {
+                tc_fence_after();
+                const Tile *t = &sh->tile[(tile_no + j) % WORDS];
+                const uint32_t part = *(volatile const uint32_t *)&t->part;
+                auto done = [&] { return x.wait(&sh->o_done[i], d_turn[i] ^ 1u, 0x472); };
+                bool ok;
+                if (part) {
+                    const uint4 w4 = *reinterpret_cast<const uint4 *>(t->word);
+                    uint32_t bits[4] = {w4.x, w4.y, w4.z, w4.w};
+                    const int first = it.np - (it.lo + j) * 8;  // group of the tile with which the draft begins
+                    if (first < 8) {
+#pragma unroll
+                        for (int g = 0; g < 8; g++) {
+                            const int d = g - first;
+                            if (d >= 0) {
+                                const uint32_t see = d < 4 ? (uint32_t)(mask >> (16 * d)) & 0xFFFFu : 0u;
+                                bits[g >> 1] &= g & 1 ? see << 16 | 0xFFFFu : see | 0xFFFF0000u;
+                            }
+                        }
+                    }
+                    auto cut_out = [&](uint32_t(&s)[4][32]) {
+#pragma unroll
+                        for (int c = 0; c < KR; c++)
+                            if (!(bits[c / 32] >> (c % 32) & 1u)) s[c / 32][c % 32] = 0xFF800000u;
+                    };
+                    ok = softmax_tile<D>(ts, to, mine == 0, qscale, m, l, &sh->p_full[i], cut_out, done);
+                } else {
+                    ok = softmax_tile<D>(ts, to, mine == 0, qscale, m, l, &sh->p_full[i], [](auto &) {}, done);
+                }
+                if (!ok) return;
+            } else if (lane == 0) {
+                mbar_arrive(&sh->p_full[i]);
+            }
+            d_turn[i] ^= 1u;
+        }
+        tile_no += n;
+        // products of the other warpgroup
+        const int theirs = two ? n : i ? (n + 1) / 2 : n / 2;
+        if (theirs & 1) d_turn[i ^ 1] ^= 1u;
+        if (mine && !x.wait(&sh->o_done[i], d_turn[i] ^ 1u, 0x473)) return;
+        float scale0 = 1.f, scale1 = 0.f;  // one tile: of O_0 and O_1
+        int c_lo = 0, c_hi = D;
+        if (!two) {
+            // join the two warpgroups' states; each finishes half of the columns
+            sh->ml[flip][i][row] = make_float2(m, l);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh->ml_full);
+            if (!x.wait(&sh->ml_full, x_turn, 0x474)) return;
+            x_turn ^= 1u;
+            if (theirs && !x.wait(&sh->o_done[i ^ 1], d_turn[i ^ 1] ^ 1u, 0x475)) return;
+            const float2 s0 = sh->ml[flip][0][row], s1 = sh->ml[flip][1][row];
+            flip ^= 1u;
+            m = fmaxf(s0.x, s1.x);
+            if (m != -INFINITY) {
+                scale0 = s0.x == m ? 1.f : ex2((s0.x - m) * qscale);
+                scale1 = s1.x == m ? 1.f : ex2((s1.x - m) * qscale);
+            }
+            l = s0.y * scale0 + s1.y * scale1;
+            c_lo = i * (D / 2);
+            c_hi = c_lo + D / 2;
+        }
+        tc_fence_after();
+        if (warp_here) {
+            const int odd = *(volatile int *)&sh->item[w.slot].odd;
+            const bool here = row < rows;
+            const bool none = m == -INFINITY && l == 0.f;
+            const int lh = it.c % a.LH;
+            const int64_t at = (int64_t)(it.t0 + node) * a.LH * a.G + (int64_t)lh * a.G + row % a.G;  // row of q and out
+            const float inv = it.rec >= 0 ? 1.f : none ? 0.f : 1.f / l;
+            float *rec = nullptr;
+            if (it.rec >= 0) rec = a.rec + ((int64_t)it.rec * a.rec_tiles + (two ? i : 0)) * (QR * (D + 2)) + row;
+#pragma unroll 1
+            for (int c = c_lo; c < c_hi; c += 32) {
+                float f[32];
+                {
+                    uint32_t o[32];
+                    tmem_ld32(o, (two ? to : o0) + c);
+                    tmem_wait_ld32(o);
+#pragma unroll
+                    for (int e = 0; e < 32; e++) f[e] = __uint_as_float(o[e]) * scale0;
+                }
+                if (!two && n > 1) {
+                    uint32_t o[32];
+                    tmem_ld32(o, o0 + D + c);
+                    tmem_wait_ld32(o);
+#pragma unroll
+                    for (int e = 0; e < 32; e++) f[e] = fmaf(__uint_as_float(o[e]), scale1, f[e]);
+                }
+                if (odd && here)
+                    for (int d = 0; d < it.nodes; d++)
+                        if (mask >> d & 1ull)
+                            add_odd(f, static_cast<const __nv_bfloat16 *>(a.v_draft) + ((int64_t)(it.t0 + d) * a.LH + lh) * D + c);
+#pragma unroll
+                for (int e = 0; e < 32; e++) f[e] *= inv;
+                if (here && rec) {
+#pragma unroll
+                    for (int e = 0; e < 32; e++) rec[(c + e) * QR] = f[e];
+                } else if (here) {
+                    store32(static_cast<__nv_bfloat16 *>(a.out) + at * D + c, f);
+                }
+                __syncwarp();
+            }
+            if (here && c_lo == 0) {
+                if (rec) {
+                    rec[D * QR] = m;
+                    rec[(D + 1) * QR] = l;
+                } else if (a.lse) {
+                    a.lse[at] = none ? -INFINITY : (m * qscale + log2f(l)) * LN2;
+                }
+            }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(&sh->o_free);
+            mbar_arrive(&sh->w_empty[w.slot]);
+        }
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(TC_THREADS, 1)
+    tree_tc_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                   const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap dk,
+                   const __grid_constant__ CUtensorMap dv) {
+    extern __shared__ unsigned char raw[];
+    __shared__ __align__(16) unsigned char sh_raw[sizeof(Shared)];
+    Shared &sh = *reinterpret_cast<Shared *>(sh_raw);
+    __shared__ uint32_t scan[33];
+    unsigned char *tiles = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    const int warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < 8; s++) {
+            mbar_init(&sh.full[s], 1);
+            mbar_init(&sh.empty[s], 1);
+            mbar_init(&sh.v_part[s], 1);
+            mbar_init(&sh.v_ready[s], 2);
+        }
+        for (int i = 0; i < 2; i++) {
+            mbar_init(&sh.q_full[i], 1);
+            mbar_init(&sh.q_empty[i], 1);
+            mbar_init(&sh.s_full[i], 1);
+            mbar_init(&sh.p_full[i], 4);
+            mbar_init(&sh.o_done[i], 1);
+            mbar_init(&sh.w_full[i], 1);
+            mbar_init(&sh.w_empty[i], 9);  // products and eight softmax warps
+        }
+        for (int i = 0; i < 4; i++) {
+            mbar_init(&sh.m_full[i], 1);
+            mbar_init(&sh.m_empty[i], 2);
+        }
+        mbar_init(&sh.o_free, 8);
+        mbar_init(&sh.ml_full, 8);
+        fence_mbar_init();
+        a.join[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    }
+    if (warp == 9) tmem_alloc(&sh.tmem, TM_COLS);
+    const bool good = load_offsets(a.cu, a.B, a.n_tokens, a.max_nodes, nullptr, a.status);
+    // work of all heads before each thread's share of them, and where this CTA's range begins
+    int n = 1;
+    if (good) {
+        const int per = ceil_div(a.C, TC_THREADS), c_lo = min(a.C, (int)threadIdx.x * per), c_hi = min(a.C, c_lo + per);
+        uint32_t sum = 0, total;
+        for (int c = c_lo; c < c_hi; c++) {
+            const Head h(a, c, nullptr);
+            sum += (uint32_t)(h.items * (h.tiles + COST));
+        }
+        uint32_t pre = block_exclusive_scan(sum, scan, &total);
+        n = max(1, min((int)gridDim.x, (int)(total / MIN_RANGE)));
+        const int i = (int)blockIdx.x, begin = i < n ? cut((int)total, i, n) : 0, end = i < n ? cut((int)total, i + 1, n) : 0;
+        if (threadIdx.x == 0) {
+            sh.begin = begin;
+            sh.end = end;
+            sh.total = (int)total;
+            sh.c0 = 0;
+            sh.p0 = 0;
+        }
+        __syncthreads();
+        if (begin < end && (uint32_t)begin >= pre && (uint32_t)begin < pre + sum)
+            for (int c = c_lo; c < c_hi; c++) {
+                const Head h(a, c, nullptr);
+                const uint32_t wgt = (uint32_t)(h.items * (h.tiles + COST));
+                if ((uint32_t)begin < pre + wgt) {
+                    sh.c0 = c;
+                    sh.p0 = (int)pre;
+                    break;
+                }
+                pre += wgt;
+            }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const Ctx<D> x{&sh, tiles, tiles + 2 * Cfg<D>::TILE, a.status};
+    if (good && sh.begin < sh.end) {
+        // 384 threads x 168 registers at launch: 256 x 208 + 128 x 80 is no more
+        if (warp < 8) {
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+            softmax_role<D>(x, a);
+        } else {
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+            if (warp == 8) load_role<D>(x, a, n, &tq, &tk, &tv, &dk, &dv);
+            else if (warp == 9) {
+                if ((threadIdx.x & 31) == 0) mma_role<D>(x, a.qscale < 0.f);
+            } else {
+                mend_role<D>(x);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(sh.tmem, TM_COLS);
+    }
+}
+
+// Joins the parts of the items that ranges' ends have cut: CTA (x, tile, 32
+// columns) those of the item whose first part CTA x had; one thread a row.
+template <int D>
+__global__ void __launch_bounds__(QR) tree_join_kernel(const TreeArgs a) {
+    const int4 d = a.join[blockIdx.x];
+    if (d.x < 0) return;
+    const int c = d.x, node0 = d.y, last = d.z, tile = blockIdx.y, col = blockIdx.z * 32, row = threadIdx.x;
+    const int b = c / a.LH, lh = c % a.LH, t0 = __ldg(a.cu + b), nodes = __ldg(a.cu + b + 1) - t0;
+    const int node = node0 + tile * a.nt + row / a.G;
+    if (row >= a.nt * a.G || node >= nodes) return;
+    const float qscale = fabsf(a.qscale);
+    const int first = (int)blockIdx.x;
+    auto rec = [&](int p) { return a.rec + ((int64_t)(2 * p + (p == first)) * a.rec_tiles + tile) * (QR * (D + 2)) + row; };
+    float m = -INFINITY;
+    for (int p = first; p <= last; p++) m = fmaxf(m, __ldcg(rec(p) + D * QR));
+    float l = 0.f, f[32];
+#pragma unroll
+    for (int e = 0; e < 32; e++) f[e] = 0.f;
+    for (int p = first; p <= last; p++) {
+        const float *r = rec(p);
+        const float mp = __ldcg(r + D * QR);
+        if (mp == -INFINITY) continue;  // the part's rows were all left out
+        const float s = mp == m ? 1.f : ex2((mp - m) * qscale);
+        l += __ldcg(r + (D + 1) * QR) * s;
+#pragma unroll
+        for (int e = 0; e < 32; e++) f[e] = fmaf(__ldcg(r + (col + e) * QR), s, f[e]);
+    }
+    const int64_t at = (int64_t)(t0 + node) * a.LH * a.G + (int64_t)lh * a.G + row % a.G;
+    const bool none = m == -INFINITY && l == 0.f;
+    const float inv = none ? 0.f : 1.f / l;
+#pragma unroll
+    for (int e = 0; e < 32; e++) f[e] *= inv;
+    store32(static_cast<__nv_bfloat16 *>(a.out) + at * D + col, f);
+    if (a.lse && col == 0) a.lse[at] = none ? -INFINITY : (m * qscale + log2f(l)) * LN2;
+}
+
+template <int D>
+cudaError_t launch(const TreeArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                   const CUtensorMap &dk, const CUtensorMap &dv, cudaStream_t s) {
+    cudaError_t e = cudaFuncSetAttribute(tree_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM);
+    if (e != cudaSuccess) return e;
+    tree_tc_kernel<D><<<TREE_CTAS, TC_THREADS, Cfg<D>::SMEM, s>>>(a, tq, tk, tv, dk, dv);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    tree_join_kernel<D><<<dim3(TREE_CTAS, a.rec_tiles, D / 32), QR, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_tree_tc(const TreeArgs &a, int D, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                           const CUtensorMap &dk, const CUtensorMap &dv, cudaStream_t s) {
+    return D == 64 ? launch<64>(a, tq, tk, tv, dk, dv, s) : launch<128>(a, tq, tk, tv, dk, dv, s);
+}
+
+}  // namespace rkv
