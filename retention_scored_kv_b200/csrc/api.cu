@@ -150,7 +150,8 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t
                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-int encode_map(CUtensorMap *m, const void *base, const cuuint64_t *dims, const cuuint64_t *strides, const cuuint32_t *box) {
+int encode_map(CUtensorMap *m, const void *base, const cuuint64_t *dims, const cuuint64_t *strides, const cuuint32_t *box,
+               int rank = 3) {
     static EncodeTiledFn fn = nullptr;
     if (!fn) {
         void *p = nullptr;
@@ -160,8 +161,8 @@ int encode_map(CUtensorMap *m, const void *base, const cuuint64_t *dims, const c
             return fail(RKV_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
         fn = reinterpret_cast<EncodeTiledFn>(p);
     }
-    const cuuint32_t estr[3] = {1, 1, 1};
-    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), dims, strides, box, estr,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(RKV_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
@@ -180,13 +181,22 @@ int encode_pool_map(CUtensorMap *m, void *pool, int D, int n_pages) {
     return encode_map(m, pool, dims, strides, box);
 }
 
+// The pool as blocks of 8 rows: (64 columns, 8 rows, D/64 planes, n_pages*2
+// blocks); one box is a page, its two blocks one after the other.
+int encode_block_map(CUtensorMap *m, const void *pool, int D, int n_pages) {
+    const cuuint32_t planes = (cuuint32_t)(D / 64);
+    const cuuint64_t dims[4] = {64, 8, planes, (cuuint64_t)n_pages * 2};
+    const cuuint64_t strides[3] = {(cuuint64_t)D * 2, 128, (cuuint64_t)D * 16};
+    const cuuint32_t box[4] = {64, 8, planes, 2};
+    return encode_map(m, pool, dims, strides, box, 4);
+}
+
 // Packed rows [n][heads][D] with `stride` elements between tokens, as (64
-// columns, n rows, heads*D/64 groups): one box is `rows` rows of `groups` groups
-// (a whole head: D/64).
-int encode_rows_map(CUtensorMap *m, const void *base, int n, int heads, int D, int64_t stride, int rows, int groups) {
+// columns, n rows, heads*D/64 groups): one box is `rows` tokens of one head.
+int encode_rows_map(CUtensorMap *m, const void *base, int n, int heads, int D, int64_t stride, int rows) {
     const cuuint64_t dims[3] = {64, (cuuint64_t)n, (cuuint64_t)heads * (D / 64)};
     const cuuint64_t strides[2] = {(cuuint64_t)stride * 2, 128};
-    const cuuint32_t box[3] = {64, (cuuint32_t)rows, (cuuint32_t)groups};
+    const cuuint32_t box[3] = {64, (cuuint32_t)rows, (cuuint32_t)(D / 64)};
     return encode_map(m, base, dims, strides, box);
 }
 
@@ -864,9 +874,9 @@ RKV_API int rkv_prompt_attn(const rkv_cache_t *cache, const int32_t *cu, int32_t
     cudaError_t e;
     if (cache->dtype == RKV_BF16) {
         CUtensorMap tq{}, tk{}, tv{};
-        if ((rc = encode_rows_map(&tq, q, n_tokens, cache->Hq, cache->D, q_stride, 128, cache->D / 64))) return rc;
-        if ((rc = encode_rows_map(&tk, k, n_tokens, cache->H, cache->D, k_stride, 128, cache->D / 64))) return rc;
-        if ((rc = encode_rows_map(&tv, v, n_tokens, cache->H, cache->D, v_stride, 128, cache->D / 64))) return rc;
+        if ((rc = encode_rows_map(&tq, q, n_tokens, cache->Hq, cache->D, q_stride, 128))) return rc;
+        if ((rc = encode_rows_map(&tk, k, n_tokens, cache->H, cache->D, k_stride, 128))) return rc;
+        if ((rc = encode_rows_map(&tv, v, n_tokens, cache->H, cache->D, v_stride, 128))) return rc;
         int sms = 0;
         if ((rc = sm_count_now(&sms))) return rc;
         e = launch_prompt_tc(a, cache->D, sms, tq, tk, tv, static_cast<cudaStream_t>(stream));
@@ -945,16 +955,16 @@ RKV_API int rkv_tree_attn(const rkv_cache_t *cache, const int32_t *cu, int32_t n
     a.qscale = attn_scale(scale);
     cudaError_t e;
     if (cache->dtype == RKV_BF16) {
-        const int D = cache->D, rows = cache->n_pages * PAGE;
+        const int D = cache->D;
         CUtensorMap tq{}, tk{}, tv{}, dk{}, dv{};
         const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a.LH * G, (cuuint64_t)n_tokens};
         const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)a.LH * G * D * 2};
         const cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)a.nt};
         if ((rc = encode_map(&tq, q, dims, strides, box))) return rc;
-        if ((rc = encode_rows_map(&tk, cache->k_pool, rows, 1, D, D, PAGE, 1))) return rc;
-        if ((rc = encode_rows_map(&tv, cache->v_pool, rows, 1, D, D, PAGE, 1))) return rc;
-        if ((rc = encode_rows_map(&dk, k_draft, n_tokens, a.LH, D, (int64_t)a.LH * D, PAGE, 1))) return rc;
-        if ((rc = encode_rows_map(&dv, v_draft, n_tokens, a.LH, D, (int64_t)a.LH * D, PAGE, 1))) return rc;
+        if ((rc = encode_block_map(&tk, cache->k_pool, D, cache->n_pages))) return rc;
+        if ((rc = encode_block_map(&tv, cache->v_pool, D, cache->n_pages))) return rc;
+        if ((rc = encode_rows_map(&dk, k_draft, n_tokens, a.LH, D, (int64_t)a.LH * D, 8))) return rc;
+        if ((rc = encode_rows_map(&dv, v_draft, n_tokens, a.LH, D, (int64_t)a.LH * D, 8))) return rc;
         e = launch_tree_tc(a, D, tq, tk, tv, dk, dv, static_cast<cudaStream_t>(stream));
     } else {
         e = launch_tree(a, cache->D, static_cast<cudaStream_t>(stream));

@@ -25,6 +25,33 @@ struct TcCfg {
     static constexpr int PLANE = 128 * 128;   // 64 columns of it
 };
 
+// Code size matters in these kernels: their roles run at the same time, and
+// beyond some 32 KB of instructions between them the SM's instruction cache
+// misses on most fetches (59 % hits measured with everything unrolled and
+// inlined, and tiles that took 5 times as long).  Hence the rolled loops, single
+// instances of the large pieces and the calls that are kept out of line.
+
+// Bounded wait on an mbarrier phase for warps that wait beside computing ones:
+// try_wait with a time hint suspends the warp until the phase ends, where polling
+// would take issue slots from the softmax warps.
+__device__ __forceinline__ bool try_wait_hint(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
+        : "memory");
+    return ok != 0;
+}
+static __device__ __noinline__ bool wait_on(uint64_t *bar, uint32_t parity, int32_t *status, int site) {
+    for (int i = 0; i < 2000; i++)
+        if (try_wait_hint(bar, parity)) return true;
+    return mbar_wait(bar, parity, status, site);
+}
+__device__ __forceinline__ bool tc_wait(uint64_t *bar, uint32_t parity, int32_t *status, int site) {
+    return try_wait_hint(bar, parity) || wait_on(bar, parity, status, site);
+}
+
 // Position in a ring of n slots and the parity of the wait for its use.
 struct Ring {
     int slot = 0;
@@ -37,52 +64,118 @@ struct Ring {
     }
 };
 
-// S = Q K^T into tensor memory.
-template <int D>
-__device__ __forceinline__ void mma_scores(uint32_t s, const void *q, const void *k, uint32_t idesc) {
-    const uint32_t q0 = smem_u32(q), k0 = smem_u32(k);
-#pragma unroll
-    for (int e = 0; e < D / 16; e++) {
-        const uint32_t off = (e / 4) * TcCfg<D>::PLANE + (e % 4) * 32;
-        mma_ss(s, tile_desc(q0 + off, 16), tile_desc(k0 + off, 16), idesc, e > 0);
-    }
+// The larger; NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
 }
 
-// O (+)= P V.
-template <int D>
-__device__ __forceinline__ void mma_output(uint32_t o, uint32_t p, const void *v, uint32_t idesc, bool first) {
-    const uint32_t v0 = smem_u32(v);
+// 2^z of a pair on the FMA pipe, for z <= 128: z = n + f with n the nearest whole
+// number (the rounding of an addition of 1.5 * 2^23), 2^f by a polynomial on
+// [-1/2, 1/2] (least-squares fit reweighted to an even relative error: 1.7e-7 in
+// fp32, as good as ex2.approx), n added to the exponent field.  Below -126 the
+// result stays at the smallest numbers.
+__device__ __forceinline__ float2 ex2_fma(float2 z) {
+    const float magic = 12582912.f;
+    z.x = fmaxf(z.x, -126.f);
+    z.y = fmaxf(z.y, -126.f);
+    const float2 t = fadd2(z, make_float2(magic, magic));
+    const float2 n = fadd2(t, make_float2(-magic, -magic));
+    const float2 f = ffma2(n, make_float2(-1.f, -1.f), z);
+    float2 p = make_float2(0.001326472731307149f, 0.001326472731307149f);
+    p = ffma2(p, f, make_float2(0.009671512991189957f, 0.009671512991189957f));
+    p = ffma2(p, f, make_float2(0.05550733581185341f, 0.05550733581185341f));
+    p = ffma2(p, f, make_float2(0.24022242426872253f, 0.24022242426872253f));
+    p = ffma2(p, f, make_float2(0.6931470036506653f, 0.6931470036506653f));
+    p = ffma2(p, f, make_float2(1.f, 1.f));
+    return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23)),
+                       __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
+}
+
+// -inf where the bit of `in` is clear.
+__device__ __forceinline__ void mask32(uint32_t (&s)[32], uint32_t in) {
 #pragma unroll
-    for (int e = 0; e < KR / 16; e++)
-        mma_ts(o, p + e * 8, tile_desc(v0 + e * 2048, TcCfg<D>::PLANE), idesc, !first || e > 0);
+    for (int e = 0; e < 32; e++) s[e] = in & (1u << e) ? s[e] : 0xFF800000u;
+}
+
+// The largest of 32 scores and mx; NaN if any is.
+__device__ __forceinline__ float max32(const uint32_t (&s)[32], float mx) {
+    float a = mx, b = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < 32; e += 4) {
+        a = max_nan(a, max_nan(__uint_as_float(s[e]), __uint_as_float(s[e + 1])));
+        b = max_nan(b, max_nan(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])));
+    }
+    return max_nan(a, b);
+}
+
+// 32 scores to weights 2^(s * qscale - ref): bf16 over the scores' place, fp32
+// into the sums.  One pair in EMU of the exponentials is computed by ex2_fma: the
+// special function unit does 16 a cycle and SM, which is what the two products of
+// a tile take as well.
+constexpr int EMU = 8;
+__device__ __forceinline__ void weights32(const uint32_t (&s)[32], uint32_t tp, float qscale, float ref, float2 (&sum)[2]) {
+    const float2 qs = make_float2(qscale, qscale), mm = make_float2(-ref, -ref);
+    uint32_t p[16];
+#pragma unroll
+    for (int e = 0; e < 16; e++) {
+        float2 z = ffma2(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), qs, mm);
+        if (e % EMU == EMU - 1) {
+            z = ex2_fma(z);
+        } else {
+            z.x = ex2(z.x);
+            z.y = ex2(z.y);
+        }
+        sum[e & 1] = fadd2(sum[e & 1], z);
+        p[e] = pack_bf16(z.x, z.y);
+    }
+    tmem_st16(tp, p);
 }
 
 // One row's S of a key tile to P.  m: the row's reference maximum of the raw
 // scores (-inf: nothing seen), l: the sum of its fp32 weights so far.  The
 // output is rescaled only when the maximum has grown by more than RESCALE: the
-// weights then stay below 2^RESCALE, far inside fp32 and bf16 range.  mask(s)
-// sets scores to -inf; done() waits for the product of the previous tile (a
-// bounded wait: false gives up).
+// weights then stay below 2^RESCALE, far inside fp32 and bf16 range.  A NaN
+// score, or one of +inf, makes the maximum and so the whole row NaN.
+// S is read twice, 32 columns at a time, once for the maximum and once for the
+// weights, instead of being held in 128 registers.  P of columns 32c..+31 lies
+// over S's 16c..+15, which are read by then.  P is handed on in halves (p_full[0],
+// [1]), so that the product of the first runs under the exponentials of the
+// second.  masked: mask(c) gives the columns of 32c..+31 that count, and the rest
+// become -inf in S.  done() waits for the product of the previous tile (a bounded
+// wait: false gives up).
 template <int D, class Mask, class Done>
 __device__ __forceinline__ bool softmax_tile(uint32_t ts, uint32_t to, bool first, float qscale, float &m, float &l,
-                                             uint64_t *p_full, Mask mask, Done done) {
-    uint32_t s[4][32];
-#pragma unroll
-    for (int c = 0; c < 4; c++) tmem_ld32(s[c], ts + c * 32);
-#pragma unroll
-    for (int c = 0; c < 4; c++) tmem_wait_ld32(s[c]);
-    mask(s);
-    float mx[4];
-#pragma unroll
-    for (int c = 0; c < 4; c++) {
-        mx[c] = __uint_as_float(s[c][0]);
-#pragma unroll
-        for (int e = 1; e < 32; e++) mx[c] = fmaxf(mx[c], __uint_as_float(s[c][e]));
+                                             uint64_t *p_full, bool masked, Mask mask, Done done) {
+    uint32_t a[32], b[32];
+    float mt = -INFINITY;
+    auto look = [&](int c, uint32_t(&s)[32]) {
+        if (masked) {
+            const uint32_t in = mask(c);
+            if (!__all_sync(0xFFFFFFFFu, in == 0xFFFFFFFFu)) {
+                mask32(s, in);
+                tmem_st32(ts + c * 32, s);
+            }
+        }
+        mt = max32(s, mt);
+    };
+    tmem_ld32(a, ts);
+#pragma unroll 1
+    for (int c = 0; c < 4; c += 2) {
+        tmem_wait_ld32(a);
+        tmem_ld32(b, ts + (c + 1) * 32);
+        look(c, a);
+        tmem_wait_ld32(b);
+        if (c == 0) tmem_ld32(a, ts + 64);
+        look(c + 1, b);
     }
-    const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-    if (__any_sync(0xFFFFFFFFu, first || (mt - m) * qscale > RESCALE)) {
+    if (masked) tmem_wait_st();
+    tmem_ld32(a, ts);
+    if (__any_sync(0xFFFFFFFFu, first || !((mt - m) * qscale <= RESCALE || mt == -INFINITY))) {
         // the whole warp moves to its new maxima (O is read and written by warps)
-        const float mn = fmaxf(m, mt);
+        float mn = max_nan(m, mt);
+        if (mn == INFINITY) mn = NAN;
         if (!first) {
             const float f = mn == -INFINITY ? 1.f : ex2((m - mn) * qscale);
             l *= f;
@@ -90,39 +183,32 @@ __device__ __forceinline__ bool softmax_tile(uint32_t ts, uint32_t to, bool firs
             tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
-                uint32_t o[32];
-                tmem_ld32(o, to + c);
-                tmem_wait_ld32(o);
+                tmem_ld32(b, to + c);
+                tmem_wait_ld32(b);
 #pragma unroll
-                for (int e = 0; e < 32; e++) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                tmem_st32(to + c, o);
+                for (int e = 0; e < 32; e++) b[e] = __float_as_uint(__uint_as_float(b[e]) * f);
+                tmem_st32(to + c, b);
             }
         }
         m = mn;
     }
     const float ref = m == -INFINITY ? 0.f : m * qscale;
-    const float2 qs = make_float2(qscale, qscale), mm = make_float2(-ref, -ref);
     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-    for (int half = 0; half < 2; half++) {
-        uint32_t p[32];
-#pragma unroll
-        for (int e = 0; e < 32; e++) {
-            const int c = half * 64 + 2 * e;
-            float2 z = ffma2(make_float2(__uint_as_float(s[c / 32][c % 32]), __uint_as_float(s[c / 32][c % 32 + 1])), qs, mm);
-            z.x = ex2(z.x);
-            z.y = ex2(z.y);
-            sum[e & 1] = fadd2(sum[e & 1], z);
-            p[e] = pack_bf16(z.x, z.y);
-        }
-        tmem_st32(ts + half * 32, p);
+#pragma unroll 1
+    for (int c = 0; c < 4; c += 2) {
+        tmem_wait_ld32(a);
+        tmem_ld32(b, ts + (c + 1) * 32);
+        weights32(a, ts + c * 16, qscale, ref, sum);
+        tmem_wait_ld32(b);
+        if (c == 0) tmem_ld32(a, ts + 64);
+        weights32(b, ts + c * 16 + 16, qscale, ref, sum);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(p_full + (c >> 1));
     }
     sum[0] = fadd2(sum[0], sum[1]);
     l += sum[0].x + sum[0].y;
-    tmem_wait_st();
-    tc_fence_before();
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(p_full);
     return true;
 }
 
@@ -145,6 +231,29 @@ __device__ __forceinline__ void store32(__nv_bfloat16 *out, const float (&f)[32]
         *reinterpret_cast<uint4 *>(out + e) =
             make_uint4(pack_bf16(f[e], f[e + 1]), pack_bf16(f[e + 2], f[e + 3]), pack_bf16(f[e + 4], f[e + 5]),
                        pack_bf16(f[e + 6], f[e + 7]));
+}
+
+// 32 columns of a warp's 32 rows of bf16 results, lane i's row at out + at (where
+// `here`): through shared memory, so that a store instruction writes 64 bytes of
+// 8 rows instead of 16 bytes of 32.  Pieces of a row are exchanged by (row / 2) mod
+// 4 against bank conflicts.  Whole warp.
+__device__ __forceinline__ void store_rows(uint4 *stage, __nv_bfloat16 *out, int64_t at, bool here, const float (&f)[32]) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t rows = __ballot_sync(0xFFFFFFFFu, here);
+#pragma unroll
+    for (int e = 0; e < 4; e++)
+        stage[lane * 4 + (e ^ (lane >> 1 & 3))] =
+            make_uint4(pack_bf16(f[8 * e], f[8 * e + 1]), pack_bf16(f[8 * e + 2], f[8 * e + 3]),
+                       pack_bf16(f[8 * e + 4], f[8 * e + 5]), pack_bf16(f[8 * e + 6], f[8 * e + 7]));
+    __syncwarp();
+#pragma unroll
+    for (int r = 0; r < 4; r++) {
+        const int row = r * 8 + lane / 4;
+        const int64_t to = __shfl_sync(0xFFFFFFFFu, at, row);
+        const uint4 v = stage[row * 4 + ((lane & 3) ^ (row >> 1 & 3))];
+        if (rows >> row & 1) *reinterpret_cast<uint4 *>(out + to + (lane & 3) * 8) = v;
+    }
+    __syncwarp();
 }
 
 // Add the infinite and NaN values among 32 columns of one row of V, which the

@@ -358,9 +358,9 @@ struct TreeLayout {
 };
 constexpr int TREE_CTAS = 148;
 TreeLayout tree_layout(int dtype, int D, int G, int64_t C, int max_nodes);
-// fp32 (tree.cu), and bf16 (tree_tc.cu) through tensor maps of the queries (nt
-// tokens x G heads), the pools' pages and the drafted tokens' K and V in groups
-// of 16, 64 columns each.
+// fp32 (tree.cu), and bf16 (tree_tc.cu) through tensor maps of the queries (64
+// columns of nt tokens x G heads), the pools' pages (two blocks of 8 rows) and
+// the drafted tokens' K and V in blocks of 8 rows.
 cudaError_t launch_tree(const TreeArgs &a, int D, cudaStream_t s);
 cudaError_t launch_tree_tc(const TreeArgs &a, int D, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                            const CUtensorMap &dk, const CUtensorMap &dv, cudaStream_t s);

@@ -23,7 +23,7 @@ namespace {
 
 template <int D>
 struct Cfg {
-    static constexpr int TILE = TcCfg<D>::TILE;
+    static constexpr int TILE = TcCfg<D>::TILE, PLANE = TcCfg<D>::PLANE;
     static constexpr int SLOTS = D == 128 ? 5 : 8;         // K and V tiles in flight
     static constexpr int SMEM = (2 + SLOTS) * TILE + 1024; // two query tiles; alignment of the swizzle's period
 };
@@ -37,7 +37,7 @@ struct Work {
 struct Shared {
     uint64_t full[8], empty[8];            // K / V slots
     uint64_t q_full[2], q_empty[2];
-    uint64_t s_full[2], p_full[2], o_done[2], o_free[2];
+    uint64_t s_full[2], p_full[2][2], o_done[2], o_free[2];  // p_full: by halves of the keys
     uint64_t v_last[8], v_ready[8];        // a slot's V of the last key tiles: loaded, and mended (full is not used)
     uint64_t w_full[2], w_empty[2];        // pieces of work
     Work work[2];
@@ -59,7 +59,7 @@ struct Ctx {
     Shared *sh;
     unsigned char *q, *kv;
     int32_t *status;
-    __device__ bool wait(uint64_t *bar, uint32_t parity, int site) const { return mbar_wait(bar, parity, status, site); }
+    __device__ bool wait(uint64_t *bar, uint32_t parity, int site) const { return tc_wait(bar, parity, status, site); }
     __device__ unsigned char *slot(int i) const { return kv + (size_t)i * Cfg<D>::TILE; }
 };
 
@@ -119,6 +119,25 @@ __device__ void load_role(const Ctx<D> &x, const PromptArgs &a, const CUtensorMa
 }
 
 // ---------------------------------------------------------- warp 9: products ----
+// S = Q K^T into tensor memory.
+template <int D>
+__device__ __forceinline__ void mma_scores(uint32_t s, uint64_t q, uint64_t k, uint32_t idesc) {
+#pragma unroll
+    for (int e = 0; e < D / 16; e++) {
+        const uint32_t off = (e / 4) * Cfg<D>::PLANE + (e % 4) * 32;
+        mma_ss(s, desc_at(q, off), desc_at(k, off), idesc, e > 0);
+    }
+}
+
+// O (+)= P V over half of the keys.
+template <int D>
+__device__ __forceinline__ void mma_output(uint32_t o, uint32_t p, uint64_t v, uint32_t idesc, int half, bool first) {
+    p += half * 32;
+    v = desc_at(v, half * 64 * 128);
+#pragma unroll
+    for (int e = 0; e < 4; e++) mma_ts(o, p + e * 8, desc_at(v, e * 2048), idesc, e > 0 || !first);
+}
+
 template <int D>
 __device__ void mma_role(const Ctx<D> &x, bool neg) {
     using C = Cfg<D>;
@@ -128,13 +147,14 @@ __device__ void mma_role(const Ctx<D> &x, bool neg) {
     Ring kv, w;
     uint32_t q_turn[2] = {0, 0}, p_turn[2] = {0, 0}, f_turn[2] = {0, 0};
     uint32_t kv_turn = 0, v_turn = 0;  // full, v_ready: a bit for each slot
+    const uint64_t q_desc = tile_desc(smem_u32(x.q), 16), k_desc = tile_desc(smem_u32(x.kv), 16),
+                   v_desc = tile_desc(smem_u32(x.kv), Cfg<D>::PLANE);
     auto scores = [&](int i, int kslot) {
-        mma_scores<D>(tmem + TM_S + i * 128, x.q + i * C::TILE, x.slot(kslot), qk);
+        mma_scores<D>(tmem + TM_S + i * 128, desc_at(q_desc, i * C::TILE), desc_at(k_desc, kslot * C::TILE), qk);
         mma_commit(&sh->s_full[i]);
     };
-    auto output = [&](int i, int vslot, bool first) {
-        mma_output<D>(tmem + TM_O + i * D, tmem + TM_S + i * 128, x.slot(vslot), pv, first);
-        mma_commit(&sh->o_done[i]);
+    auto output = [&](int i, int vslot, int half, bool first) {
+        mma_output<D>(tmem + TM_O + i * D, tmem + TM_S + i * 128, desc_at(v_desc, vslot * C::TILE), pv, half, first);
     };
     for (;; w.next(2)) {
         if (!x.wait(&sh->w_full[w.slot], w.turn, 0x410)) return;
@@ -174,10 +194,14 @@ __device__ void mma_role(const Ctx<D> &x, bool neg) {
                     if (!x.wait(&sh->o_free[i], f_turn[i] ^ 1u, 0x415)) return;
                     f_turn[i] ^= 1u;
                 }
-                if (!x.wait(&sh->p_full[i], p_turn[i], 0x416)) return;
+                if (!x.wait(&sh->p_full[i][0], p_turn[i], 0x416)) return;
+                tc_fence_after();
+                output(i, vslot, 0, j == 0);
+                if (!x.wait(&sh->p_full[i][1], p_turn[i], 0x418)) return;
                 p_turn[i] ^= 1u;
                 tc_fence_after();
-                output(i, vslot, j == 0);
+                output(i, vslot, 1, false);
+                mma_commit(&sh->o_done[i]);
                 if (j + 1 < nk) {
                     if (!k_here) {
                         if (!x.wait(&sh->full[kslot], kv_turn >> kslot & 1u, 0x417)) return;
@@ -266,14 +290,11 @@ __device__ void softmax_role(const Ctx<D> &x, const PromptArgs &a) {
                 tc_fence_after();
                 // the product of tile j - 1 has parity d_turn ^ 1 once tile j's is awaited
                 auto done = [&] { return x.wait(&sh->o_done[i], d_turn ^ 1u, 0x430); };
-                auto causal = [&](uint32_t(&s)[4][32]) {
-#pragma unroll
-                    for (int c = 0; c < KR; c++)
-                        if (c > row) s[c / 32][c % 32] = 0xFF800000u;
+                auto causal = [&](int c) {
+                    const int last = row - c * 32;  // column of the row's own token
+                    return last < 0 ? 0u : 0xFFFFFFFFu >> (31 - min(last, 31));
                 };
-                const bool ok =
-                    j + 1 == nk ? softmax_tile<D>(ts, to, j == 0, qscale, m, l, &sh->p_full[i], causal, done)
-                                : softmax_tile<D>(ts, to, j == 0, qscale, m, l, &sh->p_full[i], [](auto &) {}, done);
+                const bool ok = softmax_tile<D>(ts, to, j == 0, qscale, m, l, sh->p_full[i], j + 1 == nk, causal, done);
                 if (!ok) return;
                 d_turn ^= 1u;
             }
@@ -282,7 +303,7 @@ __device__ void softmax_role(const Ctx<D> &x, const PromptArgs &a) {
             const int r = (2 * wk.blk + i) * QR + row;  // row of the sequence
             const int odd = *(volatile int *)&sh->work[w.slot].odd;
             const bool here = r < wk.n;
-            const float inv = 1.f / l;
+            const float inv = m == -INFINITY ? NAN : 1.f / l;  // every score -inf: 0 / 0
             __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + (wk.t0 + (int64_t)r) * a.out_stride + (int64_t)wk.hq * D;
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
@@ -329,7 +350,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1) prompt_tc_kernel(const PromptAr
             mbar_init(&sh.q_full[i], 1);
             mbar_init(&sh.q_empty[i], 1);
             mbar_init(&sh.s_full[i], 1);
-            mbar_init(&sh.p_full[i], 4);
+            mbar_init(&sh.p_full[i][0], 4);
+            mbar_init(&sh.p_full[i][1], 4);
             mbar_init(&sh.o_done[i], 1);
             mbar_init(&sh.o_free[i], 4);
             mbar_init(&sh.w_full[i], 1);
@@ -343,20 +365,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1) prompt_tc_kernel(const PromptAr
     __syncthreads();
     tc_fence_after();
     const Ctx<D> x{&sh, tiles, tiles + 2 * Cfg<D>::TILE, a.status};
-    // 384 threads x 168 registers at launch: 256 x 208 + 128 x 80 is no more
     if (ok) {
-        if (warp < 8) {
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-            softmax_role<D>(x, a);
-        } else {
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-            if (warp == 8) load_role<D>(x, a, &tq, &tk, &tv);
-            else if (warp == 9) {
-                if ((threadIdx.x & 31) == 0) mma_role<D>(x, a.qscale < 0.f);
-            } else {
-                mend_role<D>(x);
-            }
-        }
+        if (warp < 8) softmax_role<D>(x, a);
+        else if (warp == 8) load_role<D>(x, a, &tq, &tk, &tv);
+        else if (warp > 9) mend_role<D>(x);
+        else if ((threadIdx.x & 31) == 0) mma_role<D>(x, a.qscale < 0.f);
     }
     tc_fence_before();
     __syncthreads();

@@ -83,14 +83,18 @@ __device__ __forceinline__ void tmem_wait_ld32(uint32_t (&r)[32]) {
 // ------------------------------------------------------------------ mma ----
 // Shared-memory matrix descriptor, 128-byte swizzle: start address, leading and
 // stride byte offsets (all in 16-byte units), descriptor version 1.
-//   rows are M or N: 8-row groups are `stride` = 1024 bytes apart; the leading
-//                    offset is unused; 16 columns further = 32 bytes further
-//   rows are K:      8-row groups 1024 bytes apart (stride), planes of 64
-//                    columns `lead` bytes apart; 16 rows further = 2048 bytes
-__device__ __forceinline__ uint64_t tile_desc(uint32_t smem_addr, uint32_t lead_bytes) {
+//   rows are M or N: 8-row groups are `stride` bytes apart; the leading offset
+//                    is unused; 16 columns further = 32 bytes further
+//   rows are K:      8-row groups `stride` bytes apart, planes of 64 columns
+//                    `lead` bytes apart
+__device__ __forceinline__ uint64_t tile_desc(uint32_t smem_addr, uint32_t lead_bytes, uint32_t stride_bytes = 1024) {
     return (uint64_t)((smem_addr >> 4) & 0x3FFFu) | (uint64_t)((lead_bytes >> 4) & 0x3FFFu) << 16 |
-           (uint64_t)(1024u >> 4) << 32 | 1ull << 46 | 2ull << 61;
+           (uint64_t)((stride_bytes >> 4) & 0x3FFFu) << 32 | 1ull << 46 | 2ull << 61;
 }
+
+// The same further on in shared memory (start addresses stay below 2^18 bytes,
+// so nothing carries into the offsets).
+__device__ __forceinline__ uint64_t desc_at(uint64_t desc, uint32_t bytes) { return desc + (bytes >> 4); }
 
 // Instruction descriptor of kind::f16: bf16 operands, fp32 accumulators, M x N;
 // `b_rows_k`: B's rows in shared memory are the reduction; `neg_a`: A negated.
@@ -127,6 +131,15 @@ __device__ __forceinline__ void tma_tile(void *smem_dst, const CUtensorMap *tmap
         "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::
             "r"(smem_u32(smem_dst)),
         "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// 4-D.
+__device__ __forceinline__ void tma_load_4d(void *smem_dst, const CUtensorMap *tmap, int x, int y, int z, int w, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::
+            "r"(smem_u32(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
         : "memory");
 }
 

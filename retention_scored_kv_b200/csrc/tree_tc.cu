@@ -15,9 +15,9 @@
 // end leaves its parts' unnormalised outputs, maxima and sums in the workspace,
 // and tree_join_kernel joins them in ascending order.
 //
-// Warps 0-7: softmax and results.  Warp 8: pages, TMA loads, keep words.  Warp 9:
-// issues the products.  Warps 10, 11: V of key tiles with rows that do not
-// count: those become zero (0 * NaN would reach every row), and infinite or NaN
+// Warps 0-7: softmax and results.  Warp 8: items, queries, K, keep words.  Warp
+// 9: issues the products.  Warp 10: V.  Warp 11: V of key tiles with rows that do
+// not count: those become zero (0 * NaN would reach every row), and infinite or NaN
 // values of drafted tokens too (not every row attends them; the results add them
 // for those that do).
 #include "attn_tc.cuh"
@@ -28,13 +28,18 @@ namespace {
 constexpr int COST = 1;       // an item's queries and results, in key tiles
 constexpr int MIN_RANGE = 4;  // key tiles of a CTA at least: a cut costs a record and a join
 constexpr int WORDS = 8;      // ring of key tiles' keep words
+constexpr int ITEMS = 4;      // ring of items
 
+// A key tile lies as its eight groups of 16 rows, each two blocks of 8 rows, each
+// D/64 planes of 8 lines of 128 bytes.  One TMA box is then a whole page (the
+// boxes' number, not their size, bounds the loads), and the 8-row blocks of a
+// tile are evenly spaced, as one descriptor needs them.
 template <int D>
 struct Cfg {
     static constexpr int TILE = TcCfg<D>::TILE, PLANE = TcCfg<D>::PLANE;
-    // K and V tiles in flight: 64 KB or more of each SM's share of HBM's latency
-    static constexpr int SLOTS = D == 128 ? 4 : 8;
-    static constexpr int SMEM = (2 + SLOTS) * TILE + 1024; // two query tiles; alignment of the swizzle's period
+    static constexpr int GROUP = PAGE * D * 2, BLOCK = GROUP / 2;
+    static constexpr int KS = D == 128 ? 2 : 4, VS = KS;  // K and V tiles in flight
+    static constexpr int SMEM = (2 + KS + VS) * TILE + 1024; // two query tiles; alignment of the swizzle's period
 };
 
 __host__ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
@@ -42,7 +47,7 @@ __host__ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b -
 struct Item {
     int c, t0, node0, nodes;  // head, first token of its sequence, first token of the item's, tokens of the sequence
     int rows[2];              // rows of the query tiles (rows[1] = 0: one tile)
-    int lo, hi, np;           // key tiles of this part; cache pages of the head
+    int lo, hi, np, len;      // key tiles of this part; cache pages and entries of the head
     int rec;                  // -1: the item is whole; else the record of this part
     int odd;                  // V of some drafted token held infinities or NaN
 };
@@ -54,19 +59,21 @@ struct __align__(16) Tile {
 };
 
 struct Mend {
-    int slot, tile, item, draft;  // draft: bit g: group g is of drafted tokens
+    int slot, item, draft;  // draft: bit g: group g is of drafted tokens
+    uint16_t word[8];
 };
 
 struct Shared {
-    uint64_t full[8], empty[8];     // K / V slots
-    uint64_t v_part[8], v_ready[8]; // a slot's V of a partial tile: loaded, and mended
+    uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
+    uint64_t v_part[4], v_ready[4]; // a slot's V of a partial tile: loaded, and mended (v_full is not used)
     uint64_t q_full[2], q_empty[2];
-    uint64_t s_full[2], p_full[2], o_done[2], o_free, ml_full;
-    uint64_t w_full[2], w_empty[2]; // items
+    uint64_t s_full[2], p_full[2][2], o_done[2], o_free, ml_full;  // p_full: by halves of the keys
+    uint64_t w_full[ITEMS], w_empty[ITEMS]; // items
     uint64_t m_full[4], m_empty[4]; // tiles to mend
-    Item item[2];
+    Item item[ITEMS];
     Tile tile[WORDS];
     Mend mend[4];
+    uint4 stage[8][32 * 4];         // results of a warp's rows, 32 columns: from a row a lane to whole lines
     float2 ml[2][2][QR];            // one-tile items: maximum and sum of both warpgroups (by item, warpgroup)
     uint32_t tmem;
     int c0, p0;                     // first head of this CTA's range and the work before it
@@ -78,22 +85,24 @@ struct Ctx {
     Shared *sh;
     unsigned char *q, *kv;
     int32_t *status;
-    __device__ bool wait(uint64_t *bar, uint32_t parity, int site) const { return mbar_wait(bar, parity, status, site); }
-    __device__ unsigned char *slot(int i) const { return kv + (size_t)i * Cfg<D>::TILE; }
+    __device__ bool wait(uint64_t *bar, uint32_t parity, int site) const { return tc_wait(bar, parity, status, site); }
+    __device__ unsigned char *k_slot(int i) const { return kv + (size_t)i * Cfg<D>::TILE; }
+    __device__ unsigned char *v_slot(int i) const { return kv + (size_t)(Cfg<D>::KS + i) * Cfg<D>::TILE; }
 };
 
 // Key tiles of head c and items it is cut into.
 struct Head {
     int t0, nodes, len, np, tiles, items;
-    __device__ Head(const TreeArgs &a, int c, int32_t *status) {
-        const int b = c / a.LH;
-        t0 = __ldg(a.cu + b);
-        nodes = __ldg(a.cu + b + 1) - t0;
-        len = clamp_len(__ldg(a.len + c), a.max_pages, status);
+    __device__ Head(const TreeArgs &a, int32_t from, int32_t to, int32_t n, int32_t *status) {
+        t0 = from;
+        nodes = to - from;
+        len = clamp_len(n, a.max_pages, status);
         np = ceil_div(len, PAGE);
         tiles = ceil_div(np + ceil_div(nodes, PAGE), 8);
         items = nodes == 0 ? 0 : nodes <= a.nt ? 1 : ceil_div(nodes, 2 * a.nt);
     }
+    __device__ Head(const TreeArgs &a, int c, int32_t *status)
+        : Head(a, __ldg(a.cu + c / a.LH), __ldg(a.cu + c / a.LH + 1), __ldg(a.len + c), status) {}
 };
 
 // Start of CTA i's range when `total` is cut into n.
@@ -106,142 +115,270 @@ __device__ __forceinline__ int cta_of(int total, int x, int n) {
     return i;
 }
 
-// ------------------------------------------------------------ warp 8: loads ----
-template <int D>
-__device__ void load_role(const Ctx<D> &x, const TreeArgs &a, int n, const CUtensorMap *tq, const CUtensorMap *tk,
-                          const CUtensorMap *tv, const CUtensorMap *dk, const CUtensorMap *dv) {
-    using C = Cfg<D>;
-    Shared *sh = x.sh;
-    const int lane = threadIdx.x & 31, cta = blockIdx.x;
-    Ring kv, w, qr, mr;
-    int tile_no = 0, pre = sh->p0;
-    bool ok = true;
-    auto wait = [&](uint64_t *bar, uint32_t parity, int site) {  // whole warp
-        int good = 1;
-        if (lane == 0) good = x.wait(bar, parity, site);
-        return __shfl_sync(0xFFFFFFFFu, good, 0) != 0;
-    };
-    for (int c = sh->c0; ok && c < a.C && pre < sh->end; c++) {
-        const Head h(a, c, a.status);
-        const int lh = c % a.LH;
-        for (int k = 0; ok && k < h.items; k++, pre += h.tiles + COST) {
-            Item it{};
-            it.lo = max(0, min(h.tiles, sh->begin - pre - COST));
-            it.hi = max(0, min(h.tiles, sh->end - pre - COST));
-            if (it.lo >= it.hi) continue;
-            it.c = c;
-            it.t0 = h.t0;
-            it.nodes = h.nodes;
-            it.np = h.np;
-            it.node0 = k * 2 * a.nt;
-            const int left = h.nodes - it.node0;
-            it.rows[0] = min(left, a.nt) * a.G;
-            it.rows[1] = left > a.nt ? min(left - a.nt, a.nt) * a.G : 0;
-            it.rec = -1;
-            if (it.lo > 0 || it.hi < h.tiles) it.rec = 2 * cta + (it.lo == 0 ? 1 : 0);
-            if (!(ok = wait(&sh->w_empty[w.slot], w.turn ^ 1u, 0x440))) break;
-            if (lane == 0) {
-                sh->item[w.slot] = it;
-                mbar_arrive(&sh->w_full[w.slot]);
-                if (it.rec >= 0 && it.lo == 0) {
-                    // this CTA has the first part: it describes the item to the join
-                    const int s = pre + COST;
-                    a.join[cta] = make_int4(c, it.node0, cta_of(sh->total, s + h.tiles - 1, n), 0);
-                }
-            }
-            // the item's one or two query tiles, behind its first key tile: their
-            // slots are free only when the products of the item before are done
-            auto queries = [&] {
-                for (int i = 0; i < (it.rows[1] ? 2 : 1); i++) {
-                    if (!wait(&sh->q_empty[qr.slot], qr.turn ^ 1u, 0x441)) return false;
-                    if (lane == 0) mbar_arrive_expect_tx(&sh->q_full[qr.slot], (uint32_t)(a.nt * a.G * D * 2));
-                    __syncwarp();
-                    if (lane < D / 64)
-                        tma_tile(x.q + qr.slot * C::TILE + lane * C::PLANE, tq, lane * 64, lh * a.G,
-                                 h.t0 + it.node0 + i * a.nt, &sh->q_full[qr.slot]);
-                    qr.next(2);
-                }
-                return true;
-            };
-            // pages and keep words of 32 groups at a time, one a lane, read a batch ahead
-            const int32_t *table = a.block_table + (int64_t)c * a.max_pages;
-            const uint16_t *keep = a.keep_mask ? a.keep_mask + (int64_t)c * a.max_pages : nullptr;
-            int32_t page = 0, next_page = 0;
-            uint32_t word = 0, next_word = 0;
-            auto fetch = [&](int u) {  // group u
-                next_page = -1;
-                next_word = 0;
-                if (u < h.np) {
-                    next_page = __ldg(table + u);
-                    next_word = keep ? __ldg(keep + u) : 0xFFFFu;
-                    const int in = h.len - u * PAGE;
-                    if (in < PAGE) next_word &= (1u << in) - 1u;
-                } else if (u - h.np < ceil_div(h.nodes, PAGE)) {
-                    const int in = h.nodes - (u - h.np) * PAGE;
-                    next_page = h.t0 + (u - h.np) * PAGE;  // a row of the draft
-                    next_word = in < PAGE ? (1u << in) - 1u : 0xFFFFu;
-                }
-            };
-            fetch(it.lo * 8 + lane);
-            for (int j = it.lo; ok && j < it.hi; j++, tile_no++) {
-                const int at = (j - it.lo) & 3;
-                if (at == 0) {
-                    page = next_page;
-                    word = next_word;
-                    const int u = j * 8 + lane;
-                    if (u < h.np && (uint32_t)page >= (uint32_t)a.n_pages) {
-                        if (word) set_status(a.status, RKV_DEV_BAD_INPUT);
-                        word = 0;
-                    }
-                    fetch(u + 32);
-                }
-                const int u = j * 8 + (lane & 7);  // lanes 0-7 (and their copies) have this tile's groups
-                const int32_t pg = __shfl_sync(0xFFFFFFFFu, page, at * 8 + (lane & 7));
-                const uint32_t wd = __shfl_sync(0xFFFFFFFFu, word, at * 8 + (lane & 7));
-                const bool draft = u >= h.np;
-                const uint32_t live = __ballot_sync(0xFFFFFFFFu, lane < 8 && wd != 0);
-                const uint32_t part = __ballot_sync(0xFFFFFFFFu, lane < 8 && (wd != 0xFFFFu || draft));
-                const uint32_t drafts = __ballot_sync(0xFFFFFFFFu, lane < 8 && wd != 0 && draft);
-                const uint32_t bytes = __popc(live) * PAGE * D * 2;
-                for (int kvi = 0; kvi < 2; kvi++) {
-                    if (!(ok = wait(&sh->empty[kv.slot], kv.turn ^ 1u, 0x442))) break;
-                    uint64_t *bar = kvi && part ? &sh->v_part[kv.slot] : &sh->full[kv.slot];
-                    if (kvi == 0) {
-                        Tile *t = &sh->tile[tile_no % WORDS];
-                        if (lane < 8) t->word[lane] = (uint16_t)wd;
-                        if (lane == 0) t->part = part;
-                    } else if (part) {
-                        if (!(ok = wait(&sh->m_empty[mr.slot], mr.turn ^ 1u, 0x443))) break;
-                        if (lane == 0) {
-                            sh->mend[mr.slot] = Mend{kv.slot, tile_no % WORDS, w.slot, (int)drafts};
-                            mbar_arrive(&sh->m_full[mr.slot]);
-                        }
-                        mr.next(4);
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
-                    __syncwarp();
-                    if (lane < 8 && wd) {
-                        unsigned char *dst = x.slot(kv.slot) + lane * PAGE * 128;
-#pragma unroll
-                        for (int p = 0; p < D / 64; p++) {
-                            if (!draft) tma_tile(dst + p * C::PLANE, kvi ? tv : tk, 0, pg * PAGE, p, bar);
-                            else tma_tile(dst + p * C::PLANE, kvi ? dv : dk, 0, pg, lh * (D / 64) + p, bar);
-                        }
-                    }
-                    kv.next(C::SLOTS);
-                }
-                if (ok && j == it.lo) ok = queries();
-            }
-            w.next(2);
+// ------------------------------------------------- warps 8 and 10: loads ----
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int32_t *status, int site) {
+    int good = 1;
+    if ((threadIdx.x & 31) == 0) good = tc_wait(bar, parity, status, site);
+    return __shfl_sync(0xFFFFFFFFu, good, 0) != 0;
+}
+
+// Whether the phase is over, without waiting; whole warp.
+__device__ __forceinline__ bool warp_test(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+    __syncwarp();
+    return ok != 0;
+}
+
+// Pages (or rows of the draft) and keep words of a head's groups of 16 rows: 32
+// of them at a time, one a lane, read a batch ahead.
+struct Groups {
+    const int32_t *table;
+    const uint16_t *keep;
+    int np, len, nodes, t0;
+    int32_t page, next_page;
+    uint32_t word, next_word;
+    __device__ void start(const TreeArgs &a, const Item &it) {
+        table = a.block_table + (int64_t)it.c * a.max_pages;
+        keep = a.keep_mask ? a.keep_mask + (int64_t)it.c * a.max_pages : nullptr;
+        np = it.np;
+        len = it.len;
+        nodes = it.nodes;
+        t0 = it.t0;
+        fetch(it.lo * 8 + (threadIdx.x & 31));
+    }
+    __device__ void fetch(int u) {
+        next_page = 0;
+        next_word = 0;
+        if (u < np) {
+            next_page = __ldg(table + u);
+            next_word = keep ? __ldg(keep + u) : 0xFFFFu;
+        } else if ((u - np) * PAGE < nodes) {
+            next_page = t0 + (u - np) * PAGE;
+            next_word = 0xFFFFu;
         }
     }
-    // the end: an item without rows, and a tile to mend without a slot
-    if (ok && wait(&sh->w_empty[w.slot], w.turn ^ 1u, 0x444) && lane == 0) {
+    // Tile j (`at`-th of this part): lanes 0-7 get its groups; whole warp.
+    __device__ void tile(int j, int at, int n_pages, int32_t *status, int32_t &pg, uint32_t &wd, bool &draft) {
+        const int lane = threadIdx.x & 31;
+        if ((at & 3) == 0) {
+            const int u = j * 8 + lane, in = u < np ? len - u * PAGE : nodes - (u - np) * PAGE;
+            page = next_page;
+            word = in < PAGE && in > 0 ? next_word & ((1u << in) - 1u) : next_word;
+            if (u < np && (uint32_t)page >= (uint32_t)n_pages) {
+                if (word) set_status(status, RKV_DEV_BAD_INPUT);
+                word = 0;
+            }
+            fetch(u + 32);
+        }
+        pg = __shfl_sync(0xFFFFFFFFu, page, (at & 3) * 8 + (lane & 7));
+        wd = __shfl_sync(0xFFFFFFFFu, word, (at & 3) * 8 + (lane & 7));
+        draft = j * 8 + (lane & 7) >= np;
+        if (lane >= 8) wd = 0;
+    }
+};
+
+// One group of 16 rows: a page, or two blocks of 8 rows of the draft.
+template <int D>
+__device__ __forceinline__ void load_group(unsigned char *dst, const CUtensorMap *pool, const CUtensorMap *draft_map, bool draft,
+                                           int32_t pg, int lh, uint64_t *bar) {
+    if (!draft) {
+        tma_load_4d(dst, pool, 0, 0, 0, pg * 2, bar);
+    } else {
+        tma_tile(dst, draft_map, 0, pg, lh * (D / 64), bar);
+        tma_tile(dst + Cfg<D>::BLOCK, draft_map, 0, pg + 8, lh * (D / 64), bar);
+    }
+}
+
+// The items of this CTA's range in order.
+struct Walk {
+    int c, k, pre;
+    __device__ bool item(const TreeArgs &a, const Shared *sh, const Head &h, Item &it) const {
+        it = Item{};
+        it.lo = max(0, min(h.tiles, sh->begin - pre - COST));
+        it.hi = max(0, min(h.tiles, sh->end - pre - COST));
+        it.c = c;
+        it.t0 = h.t0;
+        it.nodes = h.nodes;
+        it.np = h.np;
+        it.len = h.len;
+        it.node0 = k * 2 * a.nt;
+        const int left = h.nodes - it.node0;
+        it.rows[0] = min(left, a.nt) * a.G;
+        it.rows[1] = left > a.nt ? min(left - a.nt, a.nt) * a.G : 0;
+        it.rec = -1;
+        if (it.lo > 0 || it.hi < h.tiles) it.rec = 2 * (int)blockIdx.x + (it.lo == 0 ? 1 : 0);
+        return it.lo < it.hi;
+    }
+};
+
+// Warp 8: items, queries, K and the tiles' keep words.  An item's head, its first
+// pages and (where the ring has room) the item itself are read and handed on
+// while the item before it is loaded, so that short heads follow without a gap.
+template <int D>
+__device__ void load_role(const Ctx<D> &x, const TreeArgs &a, int n, const CUtensorMap *tq, const CUtensorMap *tk,
+                          const CUtensorMap *dk) {
+    using C = Cfg<D>;
+    Shared *sh = x.sh;
+    const int lane = threadIdx.x & 31;
+    Ring kr, w, qr;
+    int tile_no = 0;
+    Walk at{sh->c0, 0, sh->p0};
+    Head h(a, at.c, a.status);
+    Item it;
+    // the next item from `at` on; raw: the head after at.c is read already
+    auto seek = [&](bool raw, int32_t r0, int32_t r1, int32_t rn) {
+        for (;;) {
+            if (at.k < h.items && at.pre < sh->end) {
+                if (at.item(a, sh, h, it)) return true;
+                at.k++;
+                at.pre += h.tiles + COST;
+                continue;
+            }
+            if (++at.c >= a.C || at.pre >= sh->end) return false;
+            at.k = 0;
+            h = raw ? Head(a, r0, r1, rn, a.status) : Head(a, at.c, a.status);
+            raw = false;
+        }
+    };
+    Groups groups, ahead;
+    bool ok = true, have = seek(false, 0, 0, 0), posted = false;
+    if (have) ahead.start(a, it);
+    auto post = [&] {
+        if (lane == 0) {
+            sh->item[w.slot] = it;
+            mbar_arrive(&sh->w_full[w.slot]);
+            if (it.rec >= 0 && it.lo == 0)  // the item's first part: it describes the item to the join
+                a.join[blockIdx.x] =
+                    make_int4(it.c, it.node0, cta_of(sh->total, at.pre + COST + h.tiles - 1, n), 0);
+        }
+        w.next(ITEMS);
+        posted = true;
+    };
+    while (ok && have) {
+        if (!posted) {
+            if (!(ok = warp_wait(&sh->w_empty[w.slot], w.turn ^ 1u, a.status, 0x440))) break;
+            post();
+        }
+        posted = false;
+        const Item now = it;
+        const int lh = now.c % a.LH;
+        groups = ahead;
+        // raw lengths and offsets of the next head, used after the first tile
+        const int c2 = min(at.c + 1, a.C - 1), b2 = c2 / a.LH;
+        const int32_t r0 = __ldg(a.cu + b2), r1 = __ldg(a.cu + b2 + 1), rn = __ldg(a.len + c2);
+        for (int j = now.lo; j < now.hi; j++, tile_no++) {
+            int32_t pg;
+            uint32_t wd;
+            bool draft;
+            groups.tile(j, j - now.lo, a.n_pages, a.status, pg, wd, draft);
+            const uint32_t live = __ballot_sync(0xFFFFFFFFu, wd != 0);
+            const uint32_t part = __ballot_sync(0xFFFFFFFFu, lane < 8 && (wd != 0xFFFFu || draft));
+            if (!(ok = warp_wait(&sh->k_empty[kr.slot], kr.turn ^ 1u, a.status, 0x442))) break;
+            Tile *t = &sh->tile[tile_no % WORDS];
+            if (lane < 8) t->word[lane] = (uint16_t)wd;
+            if (lane == 0) t->part = part;
+            __syncwarp();
+            uint64_t *bar = &sh->k_full[kr.slot];
+            if (lane == 0) mbar_arrive_expect_tx(bar, __popc(live) * C::GROUP);
+            __syncwarp();
+            if (wd) load_group<D>(x.k_slot(kr.slot) + lane * C::GROUP, tk, dk, draft, pg, lh, bar);
+            kr.next(C::KS);
+            if (j > now.lo) continue;
+            // the item's one or two query tiles, behind its first key tile: their
+            // slots are free only when the products of the item before are done
+            for (int i = 0; ok && i < (now.rows[1] ? 2 : 1); i++) {
+                if (!(ok = warp_wait(&sh->q_empty[qr.slot], qr.turn ^ 1u, a.status, 0x441))) break;
+                if (lane == 0) mbar_arrive_expect_tx(&sh->q_full[qr.slot], (uint32_t)(a.nt * a.G * D * 2));
+                __syncwarp();
+                if (lane < D / 64)
+                    tma_tile(x.q + qr.slot * C::TILE + lane * C::PLANE, tq, lane * 64, lh * a.G, now.t0 + now.node0 + i * a.nt,
+                             &sh->q_full[qr.slot]);
+                qr.next(2);
+            }
+            if (!ok) break;
+            // the next item
+            at.k++;
+            at.pre += h.tiles + COST;
+            have = seek(true, r0, r1, rn);
+            if (have) {
+                ahead.start(a, it);
+                if (warp_test(&sh->w_empty[w.slot], w.turn ^ 1u)) post();
+            }
+        }
+    }
+    // the end: an item without rows
+    if (ok && warp_wait(&sh->w_empty[w.slot], w.turn ^ 1u, a.status, 0x444) && lane == 0) {
         sh->item[w.slot].rows[0] = 0;
         mbar_arrive(&sh->w_full[w.slot]);
     }
-    if (ok && wait(&sh->m_empty[mr.slot], mr.turn ^ 1u, 0x445) && lane == 0) {
+}
+
+// Warp 10: V, and the tiles whose V is to mend.
+template <int D>
+__device__ void value_role(const Ctx<D> &x, const TreeArgs &a, const CUtensorMap *tv, const CUtensorMap *dv) {
+    using C = Cfg<D>;
+    Shared *sh = x.sh;
+    const int lane = threadIdx.x & 31;
+    Ring vr, w, mr;
+    bool ok = true, early = false;
+    Groups groups, ahead;
+    for (;;) {
+        if (!early && !(ok = warp_wait(&sh->w_full[w.slot], w.turn, a.status, 0x446))) break;
+        const Item it = sh->item[w.slot];
+        if (it.rows[0] == 0) break;
+        if (early) groups = ahead;
+        else groups.start(a, it);
+        early = false;
+        Ring next = w;
+        next.next(ITEMS);
+        const int lh = it.c % a.LH;
+        for (int j = it.lo; j < it.hi; j++) {
+            int32_t pg;
+            uint32_t wd;
+            bool draft;
+            groups.tile(j, j - it.lo, a.n_pages, a.status, pg, wd, draft);
+            const uint32_t live = __ballot_sync(0xFFFFFFFFu, wd != 0);
+            const uint32_t part = __ballot_sync(0xFFFFFFFFu, lane < 8 && (wd != 0xFFFFu || draft));
+            const uint32_t drafts = __ballot_sync(0xFFFFFFFFu, wd != 0 && draft);
+            if (!(ok = warp_wait(&sh->v_empty[vr.slot], vr.turn ^ 1u, a.status, 0x447))) break;
+            uint64_t *bar = part ? &sh->v_part[vr.slot] : &sh->v_full[vr.slot];
+            if (part) {
+                if (!(ok = warp_wait(&sh->m_empty[mr.slot], mr.turn ^ 1u, a.status, 0x443))) break;
+                Mend *md = &sh->mend[mr.slot];
+                if (lane < 8) md->word[lane] = (uint16_t)wd;
+                if (lane == 0) {
+                    md->slot = vr.slot;
+                    md->item = w.slot;
+                    md->draft = (int)drafts;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh->m_full[mr.slot]);
+                mr.next(4);
+            }
+            if (lane == 0) mbar_arrive_expect_tx(bar, __popc(live) * C::GROUP);
+            __syncwarp();
+            if (wd) load_group<D>(x.v_slot(vr.slot) + lane * C::GROUP, tv, dv, draft, pg, lh, bar);
+            vr.next(C::VS);
+            if (!early && warp_test(&sh->w_full[next.slot], next.turn)) {
+                // the next item is there: its first pages
+                const Item after = sh->item[next.slot];
+                if (after.rows[0]) ahead.start(a, after);
+                early = true;
+            }
+        }
+        if (!ok) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->w_empty[w.slot]);
+        w = next;
+    }
+    // the end: a tile to mend without a slot
+    if (ok && warp_wait(&sh->m_empty[mr.slot], mr.turn ^ 1u, a.status, 0x445) && lane == 0) {
         sh->mend[mr.slot].slot = -1;
         mbar_arrive(&sh->m_full[mr.slot]);
     }
@@ -249,60 +386,71 @@ __device__ void load_role(const Ctx<D> &x, const TreeArgs &a, int n, const CUten
 
 // ---------------------------------------------------------- warp 9: products ----
 template <int D>
+__device__ __forceinline__ void mma_scores(uint32_t s, uint64_t q, uint64_t k, uint32_t idesc) {
+#pragma unroll
+    for (int e = 0; e < D / 16; e++)
+        mma_ss(s, desc_at(q, (e / 4) * Cfg<D>::PLANE + (e % 4) * 32), desc_at(k, (e / 4) * 1024 + (e % 4) * 32), idesc, e > 0);
+}
+
+template <int D>
+__device__ __forceinline__ void mma_output(uint32_t o, uint32_t p, uint64_t v, uint32_t idesc, int half, bool first) {
+    p += half * 32;
+    v = desc_at(v, half * 4 * Cfg<D>::GROUP);
+#pragma unroll
+    for (int g = 0; g < 4; g++) mma_ts(o, p + g * 8, desc_at(v, g * Cfg<D>::GROUP), idesc, g > 0 || !first);
+}
+
+template <int D>
 __device__ void mma_role(const Ctx<D> &x, bool neg) {
     using C = Cfg<D>;
     Shared *sh = x.sh;
     const uint32_t tmem = sh->tmem, qk = mma_desc(QR, KR, false, neg), pv = mma_desc(QR, D, true, false);
     Ring w, qr;
-    int kv = 0, tile_no = 0;                 // slots taken so far (mod SLOTS), key tiles so far
-    uint32_t kv_turn = 0, v_turn = 0, q_turn = 0;  // a bit for each slot
+    int kv = 0, tile_no = 0;  // key tiles so far: mod KS (and VS), in all
+    uint32_t k_turn = 0, v_turn = 0, r_turn = 0, q_turn = 0;  // k_full, v_full, v_ready, q_full: a bit for each slot
     uint32_t p_turn = 0, f_turn = 0;         // p_full: a bit for each tile; o_free
-    for (;; w.next(2)) {
+    const uint64_t q_desc = tile_desc(smem_u32(x.q), 16), k_desc = tile_desc(smem_u32(x.k_slot(0)), 16, C::BLOCK),
+                   v_desc = tile_desc(smem_u32(x.v_slot(0)), 1024, C::BLOCK);
+    for (;; w.next(ITEMS)) {
         if (!x.wait(&sh->w_full[w.slot], w.turn, 0x450)) return;
         const int rows0 = sh->item[w.slot].rows[0], rows1 = sh->item[w.slot].rows[1];
         const int n = sh->item[w.slot].hi - sh->item[w.slot].lo;
         mbar_arrive(&sh->w_empty[w.slot]);
         if (rows0 == 0) return;
         const bool two = rows1 > 0;
-        int qs[2];
+        int qs0 = qr.slot, qs1 = qr.slot;  // query tiles' slots
         for (int i = 0; i < (two ? 2 : 1); i++) {
             if (!x.wait(&sh->q_full[qr.slot], q_turn >> qr.slot & 1u, 0x451)) return;
             q_turn ^= 1u << qr.slot;
-            qs[i] = qr.slot;
+            qs1 = qr.slot;
             qr.next(2);
         }
-        if (!two) qs[1] = qs[0];
         // scores of key tile j into S_i; with two query tiles both, before its slot is given back
         auto scores = [&](int j, int i, bool wait_k, bool last) {
-            const int slot = (kv + 2 * j) % C::SLOTS;
+            const int slot = (kv + j) % C::KS;
             if (wait_k) {
-                if (!x.wait(&sh->full[slot], kv_turn >> slot & 1u, 0x452)) return false;
-                kv_turn ^= 1u << slot;
+                if (!x.wait(&sh->k_full[slot], k_turn >> slot & 1u, 0x452)) return false;
+                k_turn ^= 1u << slot;
             }
             tc_fence_after();
-            mma_scores<D>(tmem + TM_S + i * 128, x.q + qs[i] * C::TILE, x.slot(slot), qk);
+            mma_scores<D>(tmem + TM_S + i * 128, desc_at(q_desc, (i ? qs1 : qs0) * C::TILE), desc_at(k_desc, slot * C::TILE), qk);
             mma_commit(&sh->s_full[i]);
-            if (last) mma_commit(&sh->empty[slot]);
-            if (j == n - 1) {
-                if (two) mma_commit(&sh->q_empty[qs[i]]);
-                else mma_commit(&sh->q_empty[qs[0]]);
-            }
+            if (last) mma_commit(&sh->k_empty[slot]);
+            if (j == n - 1) mma_commit(&sh->q_empty[i ? qs1 : qs0]);
             return true;
         };
-        if (two) {
-            if (!scores(0, 0, true, false) || !scores(0, 1, false, true)) return;
-        } else {
-            if (!scores(0, 0, true, true) || (n > 1 && !scores(1, 1, true, true))) return;
-        }
+#pragma unroll 1
+        for (int q = 0; q < (two || n > 1 ? 2 : 1); q++)
+            if (!scores(two ? 0 : q, q, !two || q == 0, !two || q == 1)) return;
         for (int j = 0; j < n; j++) {
-            const int slot = (kv + 2 * j + 1) % C::SLOTS;
+            const int slot = (kv + j) % C::VS;
             const bool part = *(volatile uint32_t *)&sh->tile[(tile_no + j) % WORDS].part != 0;
             if (part) {
-                if (!x.wait(&sh->v_ready[slot], v_turn >> slot & 1u, 0x453)) return;
-                v_turn ^= 1u << slot;
+                if (!x.wait(&sh->v_ready[slot], r_turn >> slot & 1u, 0x453)) return;
+                r_turn ^= 1u << slot;
             } else {
-                if (!x.wait(&sh->full[slot], kv_turn >> slot & 1u, 0x454)) return;
-                kv_turn ^= 1u << slot;
+                if (!x.wait(&sh->v_full[slot], v_turn >> slot & 1u, 0x454)) return;
+                v_turn ^= 1u << slot;
             }
             if (j == 0) {
                 if (!x.wait(&sh->o_free, f_turn ^ 1u, 0x455)) return;
@@ -311,27 +459,31 @@ __device__ void mma_role(const Ctx<D> &x, bool neg) {
 #pragma unroll 1
             for (int q = 0; q < (two ? 2 : 1); q++) {
                 const int i = two ? q : j & 1;
-                if (!x.wait(&sh->p_full[i], p_turn >> i & 1u, 0x456)) return;
+                const uint32_t o = tmem + TM_O + i * D, p = tmem + TM_S + i * 128;
+                if (!x.wait(&sh->p_full[i][0], p_turn >> i & 1u, 0x456)) return;
+                tc_fence_after();
+                mma_output<D>(o, p, desc_at(v_desc, slot * C::TILE), pv, 0, two ? j == 0 : j < 2);
+                if (!x.wait(&sh->p_full[i][1], p_turn >> i & 1u, 0x457)) return;
                 p_turn ^= 1u << i;
                 tc_fence_after();
-                mma_output<D>(tmem + TM_O + i * D, tmem + TM_S + i * 128, x.slot(slot), pv, two ? j == 0 : j < 2);
+                mma_output<D>(o, p, desc_at(v_desc, slot * C::TILE), pv, 1, false);
                 mma_commit(&sh->o_done[i]);
                 const int nj = two ? j + 1 : j + 2;
                 if (nj < n && !scores(nj, i, !two || q == 0, !two || q == 1)) return;
             }
-            mma_commit(&sh->empty[slot]);
+            mma_commit(&sh->v_empty[slot]);
         }
-        kv = (kv + 2 * n) % C::SLOTS;
+        kv = (kv + n) % C::KS;
         tile_no += n;
     }
 }
 
-// ------------------------------------------------ warps 10, 11: V's odd rows ----
+// --------------------------------------------------- warp 11: V's odd rows ----
 template <int D>
 __device__ void mend_role(const Ctx<D> &x) {
     using C = Cfg<D>;
     Shared *sh = x.sh;
-    const int t = threadIdx.x - 320;
+    const int lane = threadIdx.x & 31;
     Ring mr;
     uint32_t turn = 0;  // v_part: a bit for each slot
     for (;; mr.next(4)) {
@@ -340,25 +492,38 @@ __device__ void mend_role(const Ctx<D> &x) {
         if (md.slot < 0) return;
         if (!x.wait(&sh->v_part[md.slot], turn >> md.slot & 1u, 0x461)) return;
         turn ^= 1u << md.slot;
-        uint4 *tile = reinterpret_cast<uint4 *>(x.slot(md.slot));
-        uint32_t odd = 0;
-        // 8 consecutive threads: a line of 128 bytes
-        for (int i = t; i < C::TILE / 16; i += 64) {
-            const int row = (i >> 3) & 127, g = row >> 4;
-            if (!(sh->tile[md.tile].word[g] >> (row & 15) & 1)) {
-                tile[i] = make_uint4(0, 0, 0, 0);
-            } else if (md.draft >> g & 1) {
-                uint4 v = tile[i];
-                if (drop_odd(v)) {
-                    odd = 1;
-                    tile[i] = v;
+        // a row is D/8 pieces of 16 bytes: line row % 8 of each plane of block row / 8
+        constexpr int PIECES = D / 8, ROWS = 32 / PIECES;  // rows the warp takes at once
+        const int piece = (lane / 8 % (D / 64)) * 64 + lane % 8;
+        auto at = [&](int r) {  // this lane's piece of the r-th ROWS rows of a group
+            const int row = r * ROWS + lane / PIECES;
+            return (row >> 3) * (C::BLOCK / 16) + (row & 7) * 8;
+        };
+        bool odd = false;
+        for (int g = 0; g < 8; g++) {
+            const uint32_t word = md.word[g];
+            uint4 *group = reinterpret_cast<uint4 *>(x.v_slot(md.slot) + g * C::GROUP) + piece;
+            if (md.draft >> g & 1) {
+                uint4 v[16 / ROWS];
+#pragma unroll
+                for (int r = 0; r < 16 / ROWS; r++) v[r] = group[at(r)];
+#pragma unroll
+                for (int r = 0; r < 16 / ROWS; r++) {
+                    const uint32_t keep = 0u - (word >> (r * ROWS + lane / PIECES) & 1u);
+                    v[r] = make_uint4(v[r].x & keep, v[r].y & keep, v[r].z & keep, v[r].w & keep);
+                    odd |= drop_odd(v[r]);
+                    group[at(r)] = v[r];
                 }
+            } else if (word != 0xFFFFu) {
+#pragma unroll
+                for (int r = 0; r < 16 / ROWS; r++)
+                    if (!(word >> (r * ROWS + lane / PIECES) & 1u)) group[at(r)] = make_uint4(0, 0, 0, 0);
             }
         }
         if (odd) atomicOr(&sh->item[md.item].odd, 1);
         fence_async_shared();
         __syncwarp();
-        if ((threadIdx.x & 31) == 0) {
+        if (lane == 0) {
             mbar_arrive(&sh->v_ready[md.slot]);
             mbar_arrive(&sh->m_empty[mr.slot]);
         }
@@ -377,7 +542,7 @@ __device__ void softmax_role(const Ctx<D> &x, const TreeArgs &a) {
     int tile_no = 0;
     uint32_t flip = 0;
     Ring w;
-    for (;; w.next(2)) {
+    for (;; w.next(ITEMS)) {
         if (!x.wait(&sh->w_full[w.slot], w.turn, 0x470)) return;
         const Item it = sh->item[w.slot];
         if (it.rows[0] == 0) return;
@@ -397,10 +562,13 @@ __device__ void softmax_role(const Ctx<D> &x, const TreeArgs &a) {
                 const Tile *t = &sh->tile[(tile_no + j) % WORDS];
                 const uint32_t part = *(volatile const uint32_t *)&t->part;
                 auto done = [&] { return x.wait(&sh->o_done[i], d_turn[i] ^ 1u, 0x472); };
-                bool ok;
+                uint32_t bits[4];
                 if (part) {
                     const uint4 w4 = *reinterpret_cast<const uint4 *>(t->word);
-                    uint32_t bits[4] = {w4.x, w4.y, w4.z, w4.w};
+                    bits[0] = w4.x;
+                    bits[1] = w4.y;
+                    bits[2] = w4.z;
+                    bits[3] = w4.w;
                     const int first = it.np - (it.lo + j) * 8;  // group of the tile with which the draft begins
                     if (first < 8) {
 #pragma unroll
@@ -412,18 +580,14 @@ __device__ void softmax_role(const Ctx<D> &x, const TreeArgs &a) {
                             }
                         }
                     }
-                    auto cut_out = [&](uint32_t(&s)[4][32]) {
-#pragma unroll
-                        for (int c = 0; c < KR; c++)
-                            if (!(bits[c / 32] >> (c % 32) & 1u)) s[c / 32][c % 32] = 0xFF800000u;
-                    };
-                    ok = softmax_tile<D>(ts, to, mine == 0, qscale, m, l, &sh->p_full[i], cut_out, done);
-                } else {
-                    ok = softmax_tile<D>(ts, to, mine == 0, qscale, m, l, &sh->p_full[i], [](auto &) {}, done);
                 }
+                auto columns = [&](int c) { return c < 2 ? (c ? bits[1] : bits[0]) : (c == 2 ? bits[2] : bits[3]); };
+                const bool ok =
+                    softmax_tile<D>(ts, to, mine == 0, qscale, m, l, sh->p_full[i], part != 0, columns, done);
                 if (!ok) return;
             } else if (lane == 0) {
-                mbar_arrive(&sh->p_full[i]);
+                mbar_arrive(&sh->p_full[i][0]);
+                mbar_arrive(&sh->p_full[i][1]);
             }
             d_turn[i] ^= 1u;
         }
@@ -457,7 +621,7 @@ __device__ void softmax_role(const Ctx<D> &x, const TreeArgs &a) {
         if (warp_here) {
             const int odd = *(volatile int *)&sh->item[w.slot].odd;
             const bool here = row < rows;
-            const bool none = m == -INFINITY && l == 0.f;
+            const bool none = m == -INFINITY;
             const int lh = it.c % a.LH;
             const int64_t at = (int64_t)(it.t0 + node) * a.LH * a.G + (int64_t)lh * a.G + row % a.G;  // row of q and out
             const float inv = it.rec >= 0 ? 1.f : none ? 0.f : 1.f / l;
@@ -486,13 +650,15 @@ __device__ void softmax_role(const Ctx<D> &x, const TreeArgs &a) {
                             add_odd(f, static_cast<const __nv_bfloat16 *>(a.v_draft) + ((int64_t)(it.t0 + d) * a.LH + lh) * D + c);
 #pragma unroll
                 for (int e = 0; e < 32; e++) f[e] *= inv;
-                if (here && rec) {
+                if (it.rec >= 0) {
+                    if (here) {
 #pragma unroll
-                    for (int e = 0; e < 32; e++) rec[(c + e) * QR] = f[e];
-                } else if (here) {
-                    store32(static_cast<__nv_bfloat16 *>(a.out) + at * D + c, f);
+                        for (int e = 0; e < 32; e++) rec[(c + e) * QR] = f[e];
+                    }
+                    __syncwarp();
+                } else {
+                    store_rows(sh->stage[threadIdx.x >> 5], static_cast<__nv_bfloat16 *>(a.out) + c, at * D, here, f);
                 }
-                __syncwarp();
             }
             if (here && c_lo == 0) {
                 if (rec) {
@@ -524,24 +690,27 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     unsigned char *tiles = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < 8; s++) {
-            mbar_init(&sh.full[s], 1);
-            mbar_init(&sh.empty[s], 1);
+        for (int s = 0; s < ITEMS; s++) {
+            mbar_init(&sh.w_full[s], 1);
+            mbar_init(&sh.w_empty[s], 10);  // products, V, eight softmax warps
+        }
+        for (int s = 0; s < 4; s++) {
+            mbar_init(&sh.k_full[s], 1);
+            mbar_init(&sh.k_empty[s], 1);
+            mbar_init(&sh.v_full[s], 1);
+            mbar_init(&sh.v_empty[s], 1);
             mbar_init(&sh.v_part[s], 1);
-            mbar_init(&sh.v_ready[s], 2);
+            mbar_init(&sh.v_ready[s], 1);
+            mbar_init(&sh.m_full[s], 1);
+            mbar_init(&sh.m_empty[s], 1);
         }
         for (int i = 0; i < 2; i++) {
             mbar_init(&sh.q_full[i], 1);
             mbar_init(&sh.q_empty[i], 1);
             mbar_init(&sh.s_full[i], 1);
-            mbar_init(&sh.p_full[i], 4);
+            mbar_init(&sh.p_full[i][0], 4);
+            mbar_init(&sh.p_full[i][1], 4);
             mbar_init(&sh.o_done[i], 1);
-            mbar_init(&sh.w_full[i], 1);
-            mbar_init(&sh.w_empty[i], 9);  // products and eight softmax warps
-        }
-        for (int i = 0; i < 4; i++) {
-            mbar_init(&sh.m_full[i], 1);
-            mbar_init(&sh.m_empty[i], 2);
         }
         mbar_init(&sh.o_free, 8);
         mbar_init(&sh.ml_full, 8);
@@ -587,19 +756,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     tc_fence_after();
     const Ctx<D> x{&sh, tiles, tiles + 2 * Cfg<D>::TILE, a.status};
     if (good && sh.begin < sh.end) {
-        // 384 threads x 168 registers at launch: 256 x 208 + 128 x 80 is no more
-        if (warp < 8) {
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-            softmax_role<D>(x, a);
-        } else {
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-            if (warp == 8) load_role<D>(x, a, n, &tq, &tk, &tv, &dk, &dv);
-            else if (warp == 9) {
-                if ((threadIdx.x & 31) == 0) mma_role<D>(x, a.qscale < 0.f);
-            } else {
-                mend_role<D>(x);
-            }
-        }
+        if (warp < 8) softmax_role<D>(x, a);
+        else if (warp == 8) load_role<D>(x, a, n, &tq, &tk, &dk);
+        else if (warp == 10) value_role<D>(x, a, &tv, &dv);
+        else if (warp == 11) mend_role<D>(x);
+        else if ((threadIdx.x & 31) == 0) mma_role<D>(x, a.qscale < 0.f);
     }
     tc_fence_before();
     __syncthreads();
@@ -638,7 +799,7 @@ __global__ void __launch_bounds__(QR) tree_join_kernel(const TreeArgs a) {
         for (int e = 0; e < 32; e++) f[e] = fmaf(__ldcg(r + (col + e) * QR), s, f[e]);
     }
     const int64_t at = (int64_t)(t0 + node) * a.LH * a.G + (int64_t)lh * a.G + row % a.G;
-    const bool none = m == -INFINITY && l == 0.f;
+    const bool none = m == -INFINITY;
     const float inv = none ? 0.f : 1.f / l;
 #pragma unroll
     for (int e = 0; e < 32; e++) f[e] *= inv;
