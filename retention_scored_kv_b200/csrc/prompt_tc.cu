@@ -47,9 +47,9 @@ struct Shared {
 // What a piece of work consists of: key tiles of each query tile.
 struct Shape {
     int nk0, nk1, nk;
-    __device__ Shape(const Work &w) {
-        nk0 = 2 * w.blk + 1;
-        nk1 = (2 * w.blk + 1) * QR < w.n ? nk0 + 1 : 0;
+    __device__ Shape(int blk, int n) {
+        nk0 = 2 * blk + 1;
+        nk1 = nk0 * QR < n ? nk0 + 1 : 0;
         nk = nk1 ? nk1 : nk0;
     }
 };
@@ -92,7 +92,7 @@ __device__ void load_role(const Ctx<D> &x, const PromptArgs &a, const CUtensorMa
                 mbar_arrive(&x.sh->w_full[w.slot]);
             }
             if (ok && !end) {
-                const Shape s(wk);
+                const Shape s(wk.blk, wk.n);
                 const int h = wk.hq / G, planes = D / 64;
                 auto query = [&](int i) {
                     if (!x.wait(&x.sh->q_empty[i], q_turn[i] ^ 1u, 0x401)) return false;
@@ -145,75 +145,69 @@ __device__ void mma_role(const Ctx<D> &x, bool neg) {
     const uint32_t tmem = sh->tmem;
     const uint32_t qk = mma_desc(QR, KR, false, neg), pv = mma_desc(QR, D, true, false);
     Ring kv, w;
-    uint32_t q_turn[2] = {0, 0}, p_turn[2] = {0, 0}, f_turn[2] = {0, 0};
-    uint32_t kv_turn = 0, v_turn = 0;  // full, v_ready: a bit for each slot
+    uint32_t q_turn = 0, p_turn = 0, f_turn = 0;  // q_full, p_full, o_free: a bit for each tile
+    uint32_t kv_turn = 0, v_turn = 0;             // full, v_ready: a bit for each slot
     const uint64_t q_desc = tile_desc(smem_u32(x.q), 16), k_desc = tile_desc(smem_u32(x.kv), 16),
-                   v_desc = tile_desc(smem_u32(x.kv), Cfg<D>::PLANE);
-    auto scores = [&](int i, int kslot) {
-        mma_scores<D>(tmem + TM_S + i * 128, desc_at(q_desc, i * C::TILE), desc_at(k_desc, kslot * C::TILE), qk);
-        mma_commit(&sh->s_full[i]);
-    };
-    auto output = [&](int i, int vslot, int half, bool first) {
-        mma_output<D>(tmem + TM_O + i * D, tmem + TM_S + i * 128, desc_at(v_desc, vslot * C::TILE), pv, half, first);
-    };
+                   v_desc = tile_desc(smem_u32(x.kv), C::PLANE);
     for (;; w.next(2)) {
         if (!x.wait(&sh->w_full[w.slot], w.turn, 0x410)) return;
-        const Work wk = sh->work[w.slot];
+        const int b = sh->work[w.slot].b, blk = sh->work[w.slot].blk, len = sh->work[w.slot].n;
         mbar_arrive(&sh->w_empty[w.slot]);
-        if (wk.b < 0) return;
-        const Shape s(wk);
-        int kslot = kv.slot;
-        if (!x.wait(&sh->full[kslot], kv_turn >> kslot & 1u, 0x411)) return;
-        kv_turn ^= 1u << kslot;
-        kv.next(C::SLOTS);
-        for (int i = 0; i < (s.nk1 ? 2 : 1); i++) {
-            if (!x.wait(&sh->q_full[i], q_turn[i], 0x412)) return;
-            q_turn[i] ^= 1u;
-            tc_fence_after();
-            scores(i, kslot);
-            if ((i ? s.nk1 : s.nk0) == 1) mma_commit(&sh->q_empty[i]);
-        }
-        mma_commit(&sh->empty[kslot]);
-        for (int j = 0; j < s.nk; j++) {
-            const int vslot = kv.slot;
-            if (j >= 2 * wk.blk) {
-                if (!x.wait(&sh->v_ready[vslot], v_turn >> vslot & 1u, 0x413)) return;
-                v_turn ^= 1u << vslot;
-            } else {
-                if (!x.wait(&sh->full[vslot], kv_turn >> vslot & 1u, 0x414)) return;
-                kv_turn ^= 1u << vslot;
+        if (b < 0) return;
+        const Shape s(blk, len);
+        // step j: O_i += P_i V of key tile j - 1, then S_i of key tile j
+        for (int j = 0; j <= s.nk; j++) {
+            int vslot = 0;
+            if (j > 0) {
+                vslot = kv.slot;
+                if (j - 1 >= 2 * blk) {
+                    if (!x.wait(&sh->v_ready[vslot], v_turn >> vslot & 1u, 0x413)) return;
+                    v_turn ^= 1u << vslot;
+                } else {
+                    if (!x.wait(&sh->full[vslot], kv_turn >> vslot & 1u, 0x414)) return;
+                    kv_turn ^= 1u << vslot;
+                }
+                kv.next(C::SLOTS);
             }
-            kv.next(C::SLOTS);
-            kslot = kv.slot;
+            const int kslot = kv.slot;
             bool k_here = false;
 #pragma unroll 1
             for (int i = 0; i < 2; i++) {
                 const int nk = i ? s.nk1 : s.nk0;
-                if (j >= nk) continue;
-                if (j == 0) {
-                    if (!x.wait(&sh->o_free[i], f_turn[i] ^ 1u, 0x415)) return;
-                    f_turn[i] ^= 1u;
+                if (j > nk) continue;
+                const uint32_t o = tmem + TM_O + i * D, p = tmem + TM_S + i * 128;
+                if (j > 0) {
+                    if (j == 1) {
+                        if (!x.wait(&sh->o_free[i], (f_turn >> i & 1u) ^ 1u, 0x415)) return;
+                        f_turn ^= 1u << i;
+                    }
+                    const uint64_t v = desc_at(v_desc, vslot * C::TILE);
+                    if (!x.wait(&sh->p_full[i][0], p_turn >> i & 1u, 0x416)) return;
+                    tc_fence_after();
+                    mma_output<D>(o, p, v, pv, 0, j == 1);
+                    if (!x.wait(&sh->p_full[i][1], p_turn >> i & 1u, 0x418)) return;
+                    p_turn ^= 1u << i;
+                    tc_fence_after();
+                    mma_output<D>(o, p, v, pv, 1, false);
+                    mma_commit(&sh->o_done[i]);
+                } else if (nk > 0) {
+                    if (!x.wait(&sh->q_full[i], q_turn >> i & 1u, 0x412)) return;
+                    q_turn ^= 1u << i;
                 }
-                if (!x.wait(&sh->p_full[i][0], p_turn[i], 0x416)) return;
-                tc_fence_after();
-                output(i, vslot, 0, j == 0);
-                if (!x.wait(&sh->p_full[i][1], p_turn[i], 0x418)) return;
-                p_turn[i] ^= 1u;
-                tc_fence_after();
-                output(i, vslot, 1, false);
-                mma_commit(&sh->o_done[i]);
-                if (j + 1 < nk) {
+                if (j < nk) {
                     if (!k_here) {
                         if (!x.wait(&sh->full[kslot], kv_turn >> kslot & 1u, 0x417)) return;
                         kv_turn ^= 1u << kslot;
                         k_here = true;
                     }
-                    scores(i, kslot);
-                    if (j + 2 == nk) mma_commit(&sh->q_empty[i]);
+                    tc_fence_after();
+                    mma_scores<D>(p, desc_at(q_desc, i * C::TILE), desc_at(k_desc, kslot * C::TILE), qk);
+                    mma_commit(&sh->s_full[i]);
+                    if (j + 1 == nk) mma_commit(&sh->q_empty[i]);
                 }
             }
-            mma_commit(&sh->empty[vslot]);
-            if (j + 1 < s.nk) {
+            if (j > 0) mma_commit(&sh->empty[vslot]);
+            if (j < s.nk) {
                 mma_commit(&sh->empty[kslot]);
                 kv.next(C::SLOTS);
             }
@@ -233,7 +227,7 @@ __device__ void mend_role(const Ctx<D> &x) {
         if (!x.wait(&sh->w_full[w.slot], w.turn, 0x420)) return;
         const Work wk = sh->work[w.slot];
         if (wk.b >= 0) {
-            const Shape s(wk);
+            const Shape s(wk.blk, wk.n);
             for (int j = 0; j < s.nk; j++) {
                 kv.next(C::SLOTS);  // K
                 if (j >= 2 * wk.blk) {
@@ -280,7 +274,7 @@ __device__ void softmax_role(const Ctx<D> &x, const PromptArgs &a) {
         if (!x.wait(&sh->w_full[w.slot], w.turn, 0x431)) return;
         const Work wk = sh->work[w.slot];
         if (wk.b < 0) return;
-        const Shape sp(wk);
+        const Shape sp(wk.blk, wk.n);
         const int nk = i ? sp.nk1 : sp.nk0;
         if (nk) {
             float m = -INFINITY, l = 0.f;
@@ -369,7 +363,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) prompt_tc_kernel(const PromptAr
         if (warp < 8) softmax_role<D>(x, a);
         else if (warp == 8) load_role<D>(x, a, &tq, &tk, &tv);
         else if (warp > 9) mend_role<D>(x);
-        else if ((threadIdx.x & 31) == 0) mma_role<D>(x, a.qscale < 0.f);
+        else if (elect_one()) mma_role<D>(x, a.qscale < 0.f);
     }
     tc_fence_before();
     __syncthreads();

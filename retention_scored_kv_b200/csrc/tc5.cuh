@@ -103,6 +103,17 @@ __host__ __device__ constexpr uint32_t mma_desc(int M, int N, bool b_rows_k, boo
            (uint32_t)(N / 8) << 17 | (uint32_t)(M / 16) << 24;
 }
 
+// One lane of a converged warp.  The products' issuer is chosen by it and not by
+// a comparison of the lane number: the compiler then knows that a single thread
+// runs the branch and keeps the operands in uniform registers, which the
+// instruction takes them from.  (Issuing one product took some 100 cycles
+// otherwise, longer than the product of 128 x 128 x 16 itself.)
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 // D[tmem] (+)= A[shared] * B[shared]; one thread issues for the CTA.
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
     asm volatile(

@@ -54,8 +54,6 @@ struct Item {
 
 struct __align__(16) Tile {
     uint16_t word[8];  // bit r: row r of group g counts
-    uint32_t part;     // some row does not count, or a drafted token is among them
-    uint32_t pad[3];
 };
 
 struct Mend {
@@ -72,6 +70,7 @@ struct Shared {
     uint64_t m_full[4], m_empty[4]; // tiles to mend
     Item item[ITEMS];
     Tile tile[WORDS];
+    uint32_t part[WORDS];           // some row of the tile does not count, or is of a drafted token
     Mend mend[4];
     uint4 stage[8][32 * 4];         // results of a warp's rows, 32 columns: from a row a lane to whole lines
     float2 ml[2][2][QR];            // one-tile items: maximum and sum of both warpgroups (by item, warpgroup)
@@ -280,9 +279,8 @@ __device__ void load_role(const Ctx<D> &x, const TreeArgs &a, int n, const CUten
             const uint32_t live = __ballot_sync(0xFFFFFFFFu, wd != 0);
             const uint32_t part = __ballot_sync(0xFFFFFFFFu, lane < 8 && (wd != 0xFFFFu || draft));
             if (!(ok = warp_wait(&sh->k_empty[kr.slot], kr.turn ^ 1u, a.status, 0x442))) break;
-            Tile *t = &sh->tile[tile_no % WORDS];
-            if (lane < 8) t->word[lane] = (uint16_t)wd;
-            if (lane == 0) t->part = part;
+            if (lane < 8) sh->tile[tile_no % WORDS].word[lane] = (uint16_t)wd;
+            if (lane == 0) sh->part[tile_no % WORDS] = part;
             __syncwarp();
             uint64_t *bar = &sh->k_full[kr.slot];
             if (lane == 0) mbar_arrive_expect_tx(bar, __popc(live) * C::GROUP);
@@ -404,77 +402,79 @@ template <int D>
 __device__ void mma_role(const Ctx<D> &x, bool neg) {
     using C = Cfg<D>;
     Shared *sh = x.sh;
-    const uint32_t tmem = sh->tmem, qk = mma_desc(QR, KR, false, neg), pv = mma_desc(QR, D, true, false);
+    const uint32_t tmem = sh->tmem;
+    const uint32_t qk = mma_desc(QR, KR, false, neg), pv = mma_desc(QR, D, true, false);
     Ring w, qr;
-    int kv = 0, tile_no = 0;  // key tiles so far: mod KS (and VS), in all
+    int slot0 = 0, tile_no = 0;  // key tiles so far: mod KS (and VS), mod WORDS
     uint32_t k_turn = 0, v_turn = 0, r_turn = 0, q_turn = 0;  // k_full, v_full, v_ready, q_full: a bit for each slot
-    uint32_t p_turn = 0, f_turn = 0;         // p_full: a bit for each tile; o_free
+    uint32_t p_turn = 0, f_turn = 0;                          // p_full: a bit for each tile; o_free
     const uint64_t q_desc = tile_desc(smem_u32(x.q), 16), k_desc = tile_desc(smem_u32(x.k_slot(0)), 16, C::BLOCK),
                    v_desc = tile_desc(smem_u32(x.v_slot(0)), 1024, C::BLOCK);
     for (;; w.next(ITEMS)) {
         if (!x.wait(&sh->w_full[w.slot], w.turn, 0x450)) return;
-        const int rows0 = sh->item[w.slot].rows[0], rows1 = sh->item[w.slot].rows[1];
-        const int n = sh->item[w.slot].hi - sh->item[w.slot].lo;
+        const Item *it = &sh->item[w.slot];
+        const int rows0 = it->rows[0], two = it->rows[1] > 0, n = it->hi - it->lo;
         mbar_arrive(&sh->w_empty[w.slot]);
         if (rows0 == 0) return;
-        const bool two = rows1 > 0;
         int qs0 = qr.slot, qs1 = qr.slot;  // query tiles' slots
-        for (int i = 0; i < (two ? 2 : 1); i++) {
+        for (int i = 0; i <= two; i++) {
             if (!x.wait(&sh->q_full[qr.slot], q_turn >> qr.slot & 1u, 0x451)) return;
             q_turn ^= 1u << qr.slot;
             qs1 = qr.slot;
             qr.next(2);
         }
-        // scores of key tile j into S_i; with two query tiles both, before its slot is given back
-        auto scores = [&](int j, int i, bool wait_k, bool last) {
-            const int slot = (kv + j) % C::KS;
-            if (wait_k) {
-                if (!x.wait(&sh->k_full[slot], k_turn >> slot & 1u, 0x452)) return false;
-                k_turn ^= 1u << slot;
-            }
-            tc_fence_after();
-            mma_scores<D>(tmem + TM_S + i * 128, desc_at(q_desc, (i ? qs1 : qs0) * C::TILE), desc_at(k_desc, slot * C::TILE), qk);
-            mma_commit(&sh->s_full[i]);
-            if (last) mma_commit(&sh->k_empty[slot]);
-            if (j == n - 1) mma_commit(&sh->q_empty[i ? qs1 : qs0]);
-            return true;
-        };
+        // Step t does O_i += P_i V of key tile t - ahead and S_i of key tile t: for
+        // both i with two query tiles (ahead = 1), else for i = t mod 2 (ahead = 2).
+        const int ahead = two ? 1 : 2;
 #pragma unroll 1
-        for (int q = 0; q < (two || n > 1 ? 2 : 1); q++)
-            if (!scores(two ? 0 : q, q, !two || q == 0, !two || q == 1)) return;
-        for (int j = 0; j < n; j++) {
-            const int slot = (kv + j) % C::VS;
-            const bool part = *(volatile uint32_t *)&sh->tile[(tile_no + j) % WORDS].part != 0;
-            if (part) {
-                if (!x.wait(&sh->v_ready[slot], r_turn >> slot & 1u, 0x453)) return;
-                r_turn ^= 1u << slot;
-            } else {
-                if (!x.wait(&sh->v_full[slot], v_turn >> slot & 1u, 0x454)) return;
-                v_turn ^= 1u << slot;
-            }
-            if (j == 0) {
-                if (!x.wait(&sh->o_free, f_turn ^ 1u, 0x455)) return;
-                f_turn ^= 1u;
+        for (int t = 0; t < n + ahead; t++) {
+            const int j = t - ahead, vslot = (slot0 + j + 4) % C::VS, kslot = (slot0 + t) % C::KS;
+            if (j >= 0) {
+                const int part = *(volatile uint32_t *)&sh->part[(tile_no + j) % WORDS] != 0;
+                if (part) {
+                    if (!x.wait(&sh->v_ready[vslot], r_turn >> vslot & 1u, 0x453)) return;
+                    r_turn ^= 1u << vslot;
+                } else {
+                    if (!x.wait(&sh->v_full[vslot], v_turn >> vslot & 1u, 0x454)) return;
+                    v_turn ^= 1u << vslot;
+                }
+                if (j == 0) {
+                    if (!x.wait(&sh->o_free, f_turn ^ 1u, 0x455)) return;
+                    f_turn ^= 1u;
+                }
             }
 #pragma unroll 1
-            for (int q = 0; q < (two ? 2 : 1); q++) {
-                const int i = two ? q : j & 1;
+            for (int q = 0; q <= two; q++) {
+                const int i = two ? q : t & 1;
                 const uint32_t o = tmem + TM_O + i * D, p = tmem + TM_S + i * 128;
-                if (!x.wait(&sh->p_full[i][0], p_turn >> i & 1u, 0x456)) return;
-                tc_fence_after();
-                mma_output<D>(o, p, desc_at(v_desc, slot * C::TILE), pv, 0, two ? j == 0 : j < 2);
-                if (!x.wait(&sh->p_full[i][1], p_turn >> i & 1u, 0x457)) return;
-                p_turn ^= 1u << i;
-                tc_fence_after();
-                mma_output<D>(o, p, desc_at(v_desc, slot * C::TILE), pv, 1, false);
-                mma_commit(&sh->o_done[i]);
-                const int nj = two ? j + 1 : j + 2;
-                if (nj < n && !scores(nj, i, !two || q == 0, !two || q == 1)) return;
+                if (j >= 0) {
+                    const uint64_t v = desc_at(v_desc, vslot * C::TILE);
+                    if (!x.wait(&sh->p_full[i][0], p_turn >> i & 1u, 0x456)) return;
+                    tc_fence_after();
+                    mma_output<D>(o, p, v, pv, 0, j < ahead);
+                    if (!x.wait(&sh->p_full[i][1], p_turn >> i & 1u, 0x457)) return;
+                    p_turn ^= 1u << i;
+                    tc_fence_after();
+                    mma_output<D>(o, p, v, pv, 1, false);
+                    mma_commit(&sh->o_done[i]);
+                }
+                if (t < n) {
+                    if (q == 0) {
+                        if (!x.wait(&sh->k_full[kslot], k_turn >> kslot & 1u, 0x452)) return;
+                        k_turn ^= 1u << kslot;
+                    }
+                    const int qs = q ? qs1 : qs0;
+                    tc_fence_after();
+                    mma_scores<D>(p, desc_at(q_desc, qs * C::TILE), desc_at(k_desc, kslot * C::TILE), qk);
+                    mma_commit(&sh->s_full[i]);
+                    if (q == two) mma_commit(&sh->k_empty[kslot]);
+                    if (t == n - 1) mma_commit(&sh->q_empty[qs]);
+                }
             }
-            mma_commit(&sh->v_empty[slot]);
+            if (j >= 0) mma_commit(&sh->v_empty[vslot]);
         }
-        kv = (kv + n) % C::KS;
-        tile_no += n;
+        slot0 = (slot0 + n) % C::KS;
+        tile_no = (tile_no + n) % WORDS;
     }
 }
 
@@ -560,7 +560,7 @@ __device__ void softmax_role(const Ctx<D> &x, const TreeArgs &a) {
             if (warp_here) {
                 tc_fence_after();
                 const Tile *t = &sh->tile[(tile_no + j) % WORDS];
-                const uint32_t part = *(volatile const uint32_t *)&t->part;
+                const uint32_t part = *(volatile const uint32_t *)&sh->part[(tile_no + j) % WORDS];
                 auto done = [&] { return x.wait(&sh->o_done[i], d_turn[i] ^ 1u, 0x472); };
                 uint32_t bits[4];
                 if (part) {
@@ -760,7 +760,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         else if (warp == 8) load_role<D>(x, a, n, &tq, &tk, &dk);
         else if (warp == 10) value_role<D>(x, a, &tv, &dv);
         else if (warp == 11) mend_role<D>(x);
-        else if ((threadIdx.x & 31) == 0) mma_role<D>(x, a.qscale < 0.f);
+        else if (elect_one()) mma_role<D>(x, a.qscale < 0.f);
     }
     tc_fence_before();
     __syncthreads();
