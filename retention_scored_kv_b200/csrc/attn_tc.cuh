@@ -64,11 +64,18 @@ struct Ring {
     }
 };
 
-// The larger; NaN if either is.
-__device__ __forceinline__ float max_nan(float a, float b) {
+// The largest of three; NaN if any is.  (Three operands at the rate of two.)
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
     float d;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
+}
+
+// ex2 that stays where it is written among its like.
+__device__ __forceinline__ float ex2_in_order(float x) {
+    float y;
+    asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 // -inf where the bit of `in` is clear.
@@ -79,13 +86,13 @@ __device__ __forceinline__ void mask32(uint32_t (&s)[32], uint32_t in) {
 
 // The largest of 32 scores and mx; NaN if any is.
 __device__ __forceinline__ float max32(const uint32_t (&s)[32], float mx) {
-    float a = mx, b = -INFINITY;
+    float a[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-    for (int e = 0; e < 32; e += 4) {
-        a = max_nan(a, max_nan(__uint_as_float(s[e]), __uint_as_float(s[e + 1])));
-        b = max_nan(b, max_nan(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])));
-    }
-    return max_nan(a, b);
+    for (int e = 0; e < 32; e += 8)
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            a[i] = max_nan(a[i], __uint_as_float(s[e + 2 * i]), __uint_as_float(s[e + 2 * i + 1]));
+    return max_nan(max_nan(a[0], a[1], a[2]), a[3], a[3]);
 }
 
 // 32 scores to weights 2^(s * qscale - ref): bf16 over the scores' place, fp32
@@ -94,14 +101,20 @@ __device__ __forceinline__ float max32(const uint32_t (&s)[32], float mx) {
 // 2.99 ms without, 3.03 with), since the waits between roles bound the loop.
 __device__ __forceinline__ void weights32(const uint32_t (&s)[32], uint32_t tp, float qscale, float ref, float2 (&sum)[2]) {
     const float2 qs = make_float2(qscale, qscale), mm = make_float2(-ref, -ref);
+    constexpr int LAG = 4;  // pairs between an exponential and its use: the unit's latency
+    float2 z[16];
     uint32_t p[16];
 #pragma unroll
-    for (int e = 0; e < 16; e++) {
-        float2 z = ffma2(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), qs, mm);
-        z.x = ex2(z.x);
-        z.y = ex2(z.y);
-        sum[e & 1] = fadd2(sum[e & 1], z);
-        p[e] = pack_bf16(z.x, z.y);
+    for (int e = 0; e < 16 + LAG; e++) {
+        if (e < 16) {
+            const float2 x = ffma2(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), qs, mm);
+            z[e].x = ex2_in_order(x.x);
+            z[e].y = ex2_in_order(x.y);
+        }
+        if (e >= LAG) {
+            sum[e & 1] = fadd2(sum[e & 1], z[e - LAG]);
+            p[e - LAG] = pack_bf16(z[e - LAG].x, z[e - LAG].y);
+        }
     }
     tmem_st16(tp, p);
 }
@@ -147,7 +160,7 @@ __device__ __forceinline__ bool softmax_tile(uint32_t ts, uint32_t to, bool firs
     tmem_ld32(a, ts);
     if (__any_sync(0xFFFFFFFFu, first || !((mt - m) * qscale <= RESCALE || mt == -INFINITY))) {
         // the whole warp moves to its new maxima (O is read and written by warps)
-        float mn = max_nan(m, mt);
+        float mn = max_nan(m, mt, mt);
         if (mn == INFINITY) mn = NAN;
         if (!first) {
             const float f = mn == -INFINITY ? 1.f : ex2((m - mn) * qscale);

@@ -24,7 +24,7 @@ namespace {
 template <int D>
 struct Cfg {
     static constexpr int TILE = TcCfg<D>::TILE, PLANE = TcCfg<D>::PLANE;
-    static constexpr int SLOTS = D == 128 ? 5 : 8;         // K and V tiles in flight
+    static constexpr int SLOTS = D == 128 ? 4 : 8;         // K and V tiles in flight (five measure the same)
     static constexpr int SMEM = (2 + SLOTS) * TILE + 1024; // two query tiles; alignment of the swizzle's period
 };
 
@@ -41,6 +41,7 @@ struct Shared {
     uint64_t v_last[8], v_ready[8];        // a slot's V of the last key tiles: loaded, and mended (full is not used)
     uint64_t w_full[2], w_empty[2];        // pieces of work
     Work work[2];
+    uint4 stage[8][32 * 4];                // results of a warp's rows, 32 columns
     uint32_t tmem;
 };
 
@@ -298,7 +299,7 @@ __device__ void softmax_role(const Ctx<D> &x, const PromptArgs &a) {
             const int odd = *(volatile int *)&sh->work[w.slot].odd;
             const bool here = r < wk.n;
             const float inv = m == -INFINITY ? NAN : 1.f / l;  // every score -inf: 0 / 0
-            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + (wk.t0 + (int64_t)r) * a.out_stride + (int64_t)wk.hq * D;
+            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + (int64_t)wk.hq * D;
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 uint32_t o[32];
@@ -312,8 +313,7 @@ __device__ void softmax_role(const Ctx<D> &x, const PromptArgs &a) {
                                              (int64_t)(wk.hq / (a.Hq / a.H)) * D + c;
                     for (int j = 2 * wk.blk * KR; j <= r; j++) add_odd(f, v + j * a.v_stride);
                 }
-                if (here) store32(out + c, f);
-                __syncwarp();
+                store_rows(sh->stage[threadIdx.x >> 5], out + c, (wk.t0 + (int64_t)r) * a.out_stride, here, f);
             }
             tc_fence_before();
             if (here && a.lse) a.lse[(wk.t0 + (int64_t)r) * a.Hq + wk.hq] = (m * qscale + log2f(l)) * LN2;
@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) prompt_tc_kernel(const PromptAr
                                                                const __grid_constant__ CUtensorMap tk,
                                                                const __grid_constant__ CUtensorMap tv) {
     extern __shared__ unsigned char raw[];
-    __shared__ Shared sh;
+    __shared__ __align__(16) Shared sh;
     unsigned char *tiles = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
