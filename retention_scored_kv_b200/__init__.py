@@ -383,25 +383,33 @@ def decode_step(cache: Cache, t: torch.Tensor, m_global: torch.Tensor | None, q:
                                   ctypes.c_void_p(ws.ptr), ws.nbytes, _stream(stream)))
 
 
-def _tokens(name: str, x: torch.Tensor, shape: tuple, dtype: torch.dtype, device) -> int:
-    """Address of a packed tensor [tokens, *shape]: only the token stride is free."""
-    if x.dtype != dtype or x.device != device or tuple(x.shape[1:]) != shape:
-        raise ValueError(f"{name}: {dtype} [tokens, {', '.join(map(str, shape))}] on {device} expected, got {x.dtype} "
-                         f"{tuple(x.shape)} on {x.device}")
-    n = 1
-    for size, stride in zip(reversed(shape), reversed(x.stride()[1:])):
-        if size > 1 and stride != n:
-            raise ValueError(f"{name}: the values of one token must be contiguous")
-        n *= size
+def _tokens(name: str, x: torch.Tensor, heads: int, D: int, dtype: torch.dtype, device) -> int:
+    """Address of a packed tensor [tokens, heads, D]: only the token stride is free."""
+    if x.dtype is not dtype or x.device != device or x.shape[1:] != (heads, D):
+        raise ValueError(f"{name}: {dtype} [tokens, {heads}, {D}] on {device} expected, got {x.dtype} {tuple(x.shape)} "
+                         f"on {x.device}")
+    st = x.stride()
+    if st[2] != 1 or (heads > 1 and st[1] != D):
+        raise ValueError(f"{name}: the values of one token must be contiguous")
     return x.data_ptr()
 
 
-def _packed(name: str, x: torch.Tensor, n: int, shape: tuple, dtype: torch.dtype, device) -> int:
-    """Address of a contiguous tensor [n, *shape]."""
-    if tuple(x.shape) != (n, *shape) or x.dtype != dtype or x.device != device or not x.is_contiguous():
-        raise ValueError(f"{name}: contiguous {dtype} {(n, *shape)} on {device} expected, got {x.dtype} "
-                         f"{tuple(x.shape)} on {x.device}")
+def _packed(name: str, x: torch.Tensor, shape: tuple, dtype: torch.dtype, device) -> int:
+    """Address of a contiguous tensor."""
+    if x.shape != shape or x.dtype is not dtype or x.device != device or not x.is_contiguous():
+        raise ValueError(f"{name}: contiguous {dtype} {shape} on {device} expected, got {x.dtype} {tuple(x.shape)} on "
+                         f"{x.device}")
     return x.data_ptr()
+
+
+def _on(device: torch.device, stream: torch.cuda.Stream | None, fn, *args):
+    """fn(*args, stream) on the tensors' own device, which need not be the current one; ``stream`` or that
+    device's current stream."""
+    s = stream if stream is not None else torch.cuda.current_stream(device)
+    if device.index == torch.cuda.current_device():
+        return _check(fn(*args, s.cuda_stream))
+    with torch.cuda.device(device):
+        _check(fn(*args, s.cuda_stream))
 
 
 def prompt_attn(cache: Cache, cu: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: float,
@@ -409,17 +417,14 @@ def prompt_attn(cache: Cache, cu: torch.Tensor, q: torch.Tensor, k: torch.Tensor
     """Causal attention over packed prompts, one layer: q and out [tokens, Hq, D],
     k and v [tokens, H, D] of the pool dtype (the token stride is free), cu
     int32 [B + 1], lse float32 [tokens, Hq] or None."""
-    n, dev, dt = q.shape[0], cache.len.device, cache.k_pool.dtype
+    n, dev, dt, H, Hq, D = q.shape[0], cache.len.device, cache.k_pool.dtype, cache.H, cache.Hq, cache.D
     if not n == k.shape[0] == v.shape[0] == out.shape[0]:
         raise ValueError("q, k, v and out must have the same number of tokens")
-    hq, h, i32 = (cache.Hq, cache.D), (cache.H, cache.D), torch.int32
     cs = cache.struct()
-    _check(load().rkv_prompt_attn(
-        ctypes.byref(cs), _packed("cu", cu, cache.B + 1, (), i32, dev), n,
-        _tokens("q", q, hq, dt, dev), q.stride(0), _tokens("k", k, h, dt, dev), k.stride(0),
-        _tokens("v", v, h, dt, dev), v.stride(0), float(scale), _tokens("out", out, hq, dt, dev), out.stride(0),
-        None if lse is None else _packed("lse", lse, n, (cache.Hq,), torch.float32, dev), ws.ptr, ws.nbytes,
-        _stream(stream)))
+    _on(dev, stream, load().rkv_prompt_attn, ctypes.byref(cs), _packed("cu", cu, (cache.B + 1,), torch.int32, dev), n,
+        _tokens("q", q, Hq, D, dt, dev), q.stride(0), _tokens("k", k, H, D, dt, dev), k.stride(0),
+        _tokens("v", v, H, D, dt, dev), v.stride(0), float(scale), _tokens("out", out, Hq, D, dt, dev), out.stride(0),
+        None if lse is None else _packed("lse", lse, (n, Hq), torch.float32, dev), ws.ptr, ws.nbytes)
 
 
 def append_tokens(cache: Cache, cu: torch.Tensor, pos0: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
@@ -427,16 +432,14 @@ def append_tokens(cache: Cache, cu: torch.Tensor, pos0: torch.Tensor, k_new: tor
     """Append the packed tokens of every sequence to all its heads: k_new and
     v_new [rows, L, H, D], lb_new float32 [rows, L, H]; token i is row tok[i]
     (int32), or row i without tok; positions count up from pos0[b]."""
-    n, dev, lh = k_new.shape[0], cache.len.device, (cache.L, cache.H)
+    n, dev, dt, i32, L, H = k_new.shape[0], cache.len.device, cache.k_pool.dtype, torch.int32, cache.L, cache.H
     n_new = n if tok is None else tok.shape[0]
     cs = cache.struct()
-    _check(load().rkv_append_tokens(
-        ctypes.byref(cs), _packed("cu", cu, cache.B + 1, (), torch.int32, dev),
-        None if tok is None else _packed("tok", tok, n_new, (), torch.int32, dev), n_new,
-        _packed("pos0", pos0, cache.B, (), torch.int32, dev),
-        _packed("k_new", k_new, n, (*lh, cache.D), cache.k_pool.dtype, dev),
-        _packed("v_new", v_new, n, (*lh, cache.D), cache.k_pool.dtype, dev),
-        _packed("lb_new", lb_new, n, lh, torch.float32, dev), n, ws.ptr, ws.nbytes, _stream(stream)))
+    _on(dev, stream, load().rkv_append_tokens, ctypes.byref(cs), _packed("cu", cu, (cache.B + 1,), i32, dev),
+        None if tok is None else _packed("tok", tok, (n_new,), i32, dev), n_new,
+        _packed("pos0", pos0, (cache.B,), i32, dev), _packed("k_new", k_new, (n, L, H, cache.D), dt, dev),
+        _packed("v_new", v_new, (n, L, H, cache.D), dt, dev), _packed("lb_new", lb_new, (n, L, H), torch.float32, dev),
+        n, ws.ptr, ws.nbytes)
 
 
 def tree_attn(cache: Cache, cu: torch.Tensor, q: torch.Tensor, k_draft: torch.Tensor, v_draft: torch.Tensor,
@@ -446,27 +449,23 @@ def tree_attn(cache: Cache, cu: torch.Tensor, q: torch.Tensor, k_draft: torch.Te
     [tokens, L, Hq, D], k_draft and v_draft [tokens, L, H, D] of the pool dtype,
     mask int64 [tokens] (bit j: attends drafted token j of its sequence), at
     most max_nodes tokens a sequence; ws made with at least that max_nodes."""
-    n, dev, dt, L = q.shape[0], cache.len.device, cache.k_pool.dtype, cache.L
-    cs = cache.struct()
-    _check(load().rkv_tree_attn(
-        ctypes.byref(cs), _packed("cu", cu, cache.B + 1, (), torch.int32, dev), n, int(max_nodes),
-        _packed("q", q, n, (L, cache.Hq, cache.D), dt, dev),
-        _packed("k_draft", k_draft, n, (L, cache.H, cache.D), dt, dev),
-        _packed("v_draft", v_draft, n, (L, cache.H, cache.D), dt, dev),
-        _packed("mask", mask, n, (), torch.int64, dev), float(scale),
-        ctypes.byref(sel.struct()) if sel is not None else None,
-        _packed("out", out, n, (L, cache.Hq, cache.D), dt, dev),
-        None if lse is None else _packed("lse", lse, n, (L, cache.Hq), torch.float32, dev), ws.ptr, ws.nbytes,
-        _stream(stream)))
+    n, dev, dt, L, Hq = q.shape[0], cache.len.device, cache.k_pool.dtype, cache.L, cache.Hq
+    rows, kv = (n, L, Hq, cache.D), (n, L, cache.H, cache.D)
+    cs, ss = cache.struct(), sel.struct() if sel is not None else None
+    _on(dev, stream, load().rkv_tree_attn, ctypes.byref(cs), _packed("cu", cu, (cache.B + 1,), torch.int32, dev), n,
+        int(max_nodes), _packed("q", q, rows, dt, dev), _packed("k_draft", k_draft, kv, dt, dev),
+        _packed("v_draft", v_draft, kv, dt, dev), _packed("mask", mask, (n,), torch.int64, dev), float(scale),
+        ctypes.byref(ss) if ss is not None else None, _packed("out", out, rows, dt, dev),
+        None if lse is None else _packed("lse", lse, (n, L, Hq), torch.float32, dev), ws.ptr, ws.nbytes)
 
 
 def fork_sequences(cache: Cache, parent: torch.Tensor, ws: Workspace, stream=None):
     """Slot b continues sequence parent[b] (int32 [B]; -1: the slot ends):
     pages move to one continuing slot, the others get copies."""
+    dev = cache.len.device
     cs = cache.struct()
-    _check(load().rkv_fork_sequences(ctypes.byref(cs),
-                                     _packed("parent", parent, cache.B, (), torch.int32, cache.len.device), ws.ptr,
-                                     ws.nbytes, _stream(stream)))
+    _on(dev, stream, load().rkv_fork_sequences, ctypes.byref(cs),
+        _packed("parent", parent, (cache.B,), torch.int32, dev), ws.ptr, ws.nbytes)
 
 
 @dataclass

@@ -893,9 +893,14 @@ RKV_API size_t rkv_tree_workspace_size(const rkv_cache_t *cache, int32_t max_nod
         fail(RKV_ERR_INVALID_ARG, "max_nodes must be in [1, %d]", TREE_MAX_NODES);
         return 0;
     }
-    size_t ticket, rec, total;
-    tree_offsets(*cache, max_nodes, &ticket, &rec, &total);
-    return total;
+    // enough for every smaller tree too, whose layout need not be smaller
+    size_t most = 0;
+    for (int n = 1; n <= max_nodes; n++) {
+        size_t ticket, rec, total;
+        tree_offsets(*cache, n, &ticket, &rec, &total);
+        most = total > most ? total : most;
+    }
+    return most;
 }
 
 RKV_API int rkv_tree_attn(const rkv_cache_t *cache, const int32_t *cu, int32_t n_tokens, int32_t max_nodes,
@@ -948,6 +953,7 @@ RKV_API int rkv_tree_attn(const rkv_cache_t *cache, const int32_t *cu, int32_t n
     a.n_pages = cache->n_pages;
     a.n_tokens = n_tokens;
     a.max_nodes = max_nodes;
+    a.row_tile = tl.rows;
     a.row_tiles = tl.row_tiles;
     a.parts = tl.parts;
     a.nt = tl.nt;

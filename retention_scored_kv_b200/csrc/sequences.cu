@@ -17,104 +17,126 @@ __device__ __forceinline__ int pages_of(int n) { return (n + PAGE - 1) / PAGE; }
 // ascending order.  base[c] = its length before the call (-1: the head takes
 // nothing), pop[c] = index of its first page on the free stack (later ones
 // below it).  A head that would leave its table takes no page; one that finds
-// too few pages is skipped, and so is every later head that needs one.
+// too few pages is skipped, and so is every later head that needs one.  Each
+// thread has a run of consecutive heads, so that one scan does for all.
 __global__ void __launch_bounds__(PLAN_THREADS) append_plan_kernel(const AppendTokensArgs a) {
     extern __shared__ int32_t s_cu[];
     __shared__ uint32_t scan[33];
     __shared__ int s_short;
+    launch_dependents();
     if (threadIdx.x == 0) {
         s_short = INT32_MAX;
         a.plan[0] = 0;
     }
     if (!load_offsets(a.cu, a.B, a.n_new, a.n_new, s_cu, a.status)) return;
     const int top = min(max(*a.free_top, 0), a.n_pages);
-    uint32_t taken = 0;
-    for (int c0 = 0; c0 < a.C; c0 += PLAN_THREADS) {
-        const int c = c0 + threadIdx.x;
-        int len = 0, n = 0, need = 0, bits = 0;
-        if (c < a.C) {
-            const int b = c / a.LH;
-            n = s_cu[b + 1] - s_cu[b];
-            len = a.len[c];
-            if (len < 0) bits = RKV_DEV_BAD_INPUT;
-            else if ((int64_t)len + n > (int64_t)a.max_pages * PAGE) bits = RKV_DEV_TABLE_OVERFLOW;
-            const int32_t p0 = __ldg(a.pos0 + b);
-            if (n > 0 && (p0 < 0 || (int64_t)p0 + n > INT32_MAX)) bits = RKV_DEV_BAD_INPUT;
-            if (n == 0) bits = 0;
-            if (!bits) need = pages_of(len + n) - pages_of(len);
-        }
-        uint32_t total;
-        const uint32_t before = taken + block_exclusive_scan((uint32_t)need, scan, &total);
+    const int per = (a.C + PLAN_THREADS - 1) / PLAN_THREADS, c0 = min(a.C, (int)threadIdx.x * per), c1 = min(a.C, c0 + per);
+    // pages that head c needs; -1: the head takes nothing (bits: why)
+    auto look = [&](int c, int &len, int &n, int &bits) {
+        const int b = c / a.LH;
+        n = s_cu[b + 1] - s_cu[b];
+        len = a.len[c];
+        bits = 0;
+        if (n == 0) return -1;
+        const int32_t p0 = __ldg(a.pos0 + b);
+        if (len < 0 || p0 < 0 || (int64_t)p0 + n > INT32_MAX) bits = RKV_DEV_BAD_INPUT;
+        else if ((int64_t)len + n > (int64_t)a.max_pages * PAGE) bits = RKV_DEV_TABLE_OVERFLOW;
+        return bits ? -1 : pages_of(len + n) - pages_of(len);
+    };
+    uint32_t sum = 0, total;
+    for (int c = c0; c < c1; c++) {
+        int len, n, bits;
+        sum += (uint32_t)max(0, look(c, len, n, bits));
+    }
+    uint32_t before = block_exclusive_scan(sum, scan, &total);
+    for (int c = c0; c < c1; c++) {
+        int len, n, bits;
+        const int need = look(c, len, n, bits);
         if (need > 0 && (int64_t)before + need > (int64_t)top) {
             bits = RKV_DEV_POOL_EXHAUSTED;
             atomicMin(&s_short, (int)before);  // pages taken by the heads before the first that fails
         }
-        if (c < a.C) {
-            const bool ok = !bits && n > 0;
-            a.base[c] = ok ? len : -1;
-            a.pop[c] = top - 1 - (int)before;
-            if (ok) a.len[c] = len + n;
-            if (bits) set_status(a.status, bits);
-        }
-        taken += total;
+        const bool ok = need >= 0 && !bits;
+        a.base[c] = ok ? len : -1;
+        a.pop[c] = top - 1 - (int)before;
+        if (ok) a.len[c] = len + n;
+        if (bits) set_status(a.status, bits);
+        before += (uint32_t)max(0, need);
     }
     __syncthreads();
     if (threadIdx.x == 0) {
-        *a.free_top = top - (int)min((uint32_t)s_short, taken);
+        *a.free_top = top - (int)min((uint32_t)s_short, total);
         a.plan[0] = 1;
     }
 }
 
-// Rows of all heads in order (head, token): a warp takes 32 of them.  Lane i
-// finds where row i goes (its page is in the table, or the head's next one on
-// the stack, which is then entered in the table); the warp then copies the 32
-// K and V rows in 16-byte pieces.
+// A warp takes 32 tokens of one head; the warps of a CTA and the CTAs in order
+// take neighbouring heads of the same tokens, whose rows are neighbours in k_new
+// and v_new (in the order of one head's tokens the reads are 256 bytes in every
+// 64 KB).  Lane i finds where token i goes (its page is in the table, or the
+// head's next one on the stack, which is then entered in the table); the warp
+// then copies the rows in 16-byte pieces.
 constexpr int MOVE_THREADS = 256;
 template <int CH>  // 16-byte pieces of a row
-__global__ void __launch_bounds__(MOVE_THREADS) append_rows_kernel(const AppendTokensArgs a) {
-    extern __shared__ int32_t s_cu[];
+__global__ void __launch_bounds__(MOVE_THREADS, 4) append_rows_kernel(const AppendTokensArgs a) {
+    extern __shared__ int32_t s_cu[];  // offsets, then blocks of 32 tokens before each sequence
+    __shared__ uint32_t scan[33];
+    wait_for_launcher();
     if (a.plan[0] == 0) return;
-    for (int i = threadIdx.x; i <= a.B; i += MOVE_THREADS) s_cu[i] = __ldg(a.cu + i);
+    int32_t *s_pre = s_cu + a.B + 1;
+    const int per = (a.B + MOVE_THREADS - 1) / MOVE_THREADS;
+    const int q0 = min(a.B, (int)threadIdx.x * per), q1 = min(a.B, q0 + per);
+    uint32_t sum = 0, blocks;
+    for (int q = q0; q < q1; q++) sum += (uint32_t)(__ldg(a.cu + q + 1) - __ldg(a.cu + q) + 31) / 32;
+    uint32_t pre = block_exclusive_scan(sum, scan, &blocks);
+    for (int q = q0; q < q1; q++) {
+        s_cu[q] = __ldg(a.cu + q);
+        s_pre[q] = (int32_t)pre;
+        pre += (uint32_t)(__ldg(a.cu + q + 1) - s_cu[q] + 31) / 32;
+    }
+    if (threadIdx.x == 0) s_cu[a.B] = __ldg(a.cu + a.B);
     __syncthreads();
     const int lane = threadIdx.x & 31;
-    const int64_t warps = (int64_t)gridDim.x * (MOVE_THREADS / 32);
-    const int64_t rows = (int64_t)(s_cu[a.B] - s_cu[0]) * a.LH;
-    int b = 0;
-    for (int64_t g = ((int64_t)blockIdx.x * (MOVE_THREADS / 32) + (threadIdx.x >> 5)) * 32; g < rows; g += warps * 32) {
-        const int64_t i = g + lane;
+    const int64_t warps = (int64_t)gridDim.x * (MOVE_THREADS / 32), groups = (int64_t)blocks * a.LH;
+    for (int64_t g = (int64_t)blockIdx.x * (MOVE_THREADS / 32) + (threadIdx.x >> 5); g < groups; g += warps) {
+        const int block = (int)(g / a.LH), lh = (int)(g % a.LH);
+        int b = 0, hi = a.B;  // the last sequence with s_pre <= block that is not empty
+        while (hi - b > 1) {
+            const int mid = (b + hi) >> 1;
+            if (s_pre[mid] <= block) b = mid;
+            else hi = mid;
+        }
+        const int j0 = (block - s_pre[b]) * 32, n = min(32, s_cu[b + 1] - s_cu[b] - j0);
+        const int c = b * a.LH + lh, base = a.base[c];
+        if (base < 0) continue;
         int64_t dst = -1, src = 0;
-        if (i < rows) {
-            while ((int64_t)(s_cu[b + 1] - s_cu[0]) * a.LH <= i) b++;
-            const int64_t r = i - (int64_t)(s_cu[b] - s_cu[0]) * a.LH;
-            const int n = s_cu[b + 1] - s_cu[b], lh = (int)(r / n), j = (int)(r % n);
-            const int c = b * a.LH + lh, base = a.base[c];
+        if (lane < n) {
+            const int j = j0 + lane, slot = base + j, p = slot / PAGE, have = pages_of(base);
             int64_t row = s_cu[b] + j;
             if (a.tok) row = __ldg(a.tok + row);
-            if (base >= 0) {
-                const int slot = base + j, p = slot / PAGE, have = pages_of(base);
-                int32_t *entry = a.block_table + (int64_t)c * a.max_pages + p;
-                const int32_t page = p < have ? *entry : a.free_stack[a.pop[c] - (p - have)];
-                if (p >= have && slot % PAGE == 0) *entry = page;
-                if (page < 0 || page >= a.n_pages || row < 0 || row >= a.n_rows) {
-                    set_status(a.status, RKV_DEV_BAD_INPUT);
-                } else {
-                    src = row * a.LH + lh;
-                    dst = (int64_t)page * PAGE + slot % PAGE;
-                    a.pos_pool[dst] = __ldg(a.pos0 + b) + j;
-                    a.lb_pool[dst] = __ldg(a.lb_new + src);
-                }
+            int32_t *entry = a.block_table + (int64_t)c * a.max_pages + p;
+            const int32_t page = p < have ? *entry : a.free_stack[a.pop[c] - (p - have)];
+            if (p >= have && slot % PAGE == 0) *entry = page;
+            if (page < 0 || page >= a.n_pages || row < 0 || row >= a.n_rows) {
+                set_status(a.status, RKV_DEV_BAD_INPUT);
+            } else {
+                src = row * a.LH + lh;
+                dst = (int64_t)page * PAGE + slot % PAGE;
+                a.pos_pool[dst] = __ldg(a.pos0 + b) + j;
+                a.lb_pool[dst] = __ldg(a.lb_new + src);
             }
         }
-        constexpr int PER = 32 / CH, UN = 8;  // rows a warp moves at once, steps in flight
+        constexpr int PER = 32 / CH, UN = 4;  // rows a warp moves at once, steps in flight
 #pragma unroll 1
-        for (int k0 = 0; k0 < 32; k0 += PER * UN) {
+        for (int k0 = 0; k0 < n; k0 += PER * UN) {
             uint4 xk[UN], xv[UN];
             int64_t to[UN];
 #pragma unroll
             for (int u = 0; u < UN; u++) {
-                const int k = (k0 + u * PER + lane / CH) & 31;
-                to[u] = __shfl_sync(0xFFFFFFFFu, dst, k);
-                const int64_t from = __shfl_sync(0xFFFFFFFFu, src, k);
+                const int k = k0 + u * PER + lane / CH;
+                to[u] = __shfl_sync(0xFFFFFFFFu, dst, k & 31);
+                const int64_t from = __shfl_sync(0xFFFFFFFFu, src, k & 31);
+                if (k >= 32) to[u] = -1;
                 if (to[u] >= 0) {
                     xk[u] = __ldcs(static_cast<const uint4 *>(a.k_new) + from * CH + lane % CH);
                     xv[u] = __ldcs(static_cast<const uint4 *>(a.v_new) + from * CH + lane % CH);
@@ -146,6 +168,7 @@ __device__ __forceinline__ int heir_of(const int32_t *parent, int B, int s) {
 __global__ void __launch_bounds__(PLAN_THREADS) fork_plan_kernel(const ForkArgs a) {
     __shared__ int32_t s_par[FORK_MAX_B], s_heir[FORK_MAX_B];
     __shared__ uint32_t scan[33];
+    launch_dependents();
     if (blockIdx.x == 0 && threadIdx.x == 0) a.plan[0] = 0;
     int bad = 0;
     if (threadIdx.x < a.B) {
@@ -215,6 +238,7 @@ template <int CH>
 __global__ void __launch_bounds__(FORK_THREADS) fork_rows_kernel(const ForkArgs a) {
     __shared__ int32_t s_par[FORK_MAX_B], s_heir[FORK_MAX_B], s_n[FORK_MAX_B], s_pop[FORK_MAX_B];
     __shared__ int32_t s_old[FORK_MAX_B][FORK_COLS], s_new[FORK_MAX_B][FORK_COLS];
+    wait_for_launcher();
     if (a.plan[0] == 0) return;
     const int blocks = (a.max_pages + FORK_COLS - 1) / FORK_COLS;
     const int lh = blockIdx.x / blocks, p0 = blockIdx.x % blocks * FORK_COLS;
@@ -296,18 +320,17 @@ __global__ void __launch_bounds__(FORK_THREADS) fork_rows_kernel(const ForkArgs 
 
 template <int CH>
 cudaError_t append_rows(const AppendTokensArgs &a, cudaStream_t s) {
-    const int64_t groups = ((int64_t)a.n_new * a.LH + 31) / 32, per = MOVE_THREADS / 32;
+    const int64_t groups = ((int64_t)a.n_new / 32 + a.B) * a.LH, per = MOVE_THREADS / 32;  // at most
     const int64_t ctas = (groups + per - 1) / per;
-    append_rows_kernel<CH><<<(unsigned)(ctas < 148 * 8 ? ctas : 148 * 8), MOVE_THREADS, (a.B + 1) * 4, s>>>(a);
-    return cudaGetLastError();
+    return launch_after(append_rows_kernel<CH>, (unsigned)(ctas < 148 * 4 ? ctas : 148 * 4), MOVE_THREADS,
+                        (size_t)(2 * a.B + 1) * 4, s, a);
 }
 
 template <int CH>
 cudaError_t fork_rows(const ForkArgs &a, cudaStream_t s) {
     const int64_t ctas = (int64_t)a.LH * ((a.max_pages + FORK_COLS - 1) / FORK_COLS);
     if (ctas >= (1ll << 31)) return cudaErrorNotSupported;
-    fork_rows_kernel<CH><<<(unsigned)ctas, FORK_THREADS, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_after(fork_rows_kernel<CH>, (unsigned)ctas, FORK_THREADS, 0, s, a);
 }
 
 }  // namespace

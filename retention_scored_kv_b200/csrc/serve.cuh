@@ -9,6 +9,28 @@ namespace rkv {
 
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
+// --------------------------------------------------- launches in pairs ----
+// The second kernel of a pair is set up while the first still runs
+// (launch_dependents in the first, launch_after on the host) and waits for its
+// end, and for its writes, at wait_for_launcher.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_launcher() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <class Args>
+cudaError_t launch_after(void (*kernel)(Args), dim3 grid, unsigned threads, size_t smem, cudaStream_t s, const Args &a) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
 // ------------------------------------------------------ packed sequences ----
 // Copies the offsets cu[0..B] to shared memory (unless NULL) and checks them: non-negative,
 // non-decreasing, cu[B] <= n_tokens and no sequence longer than `longest`.
@@ -75,29 +97,34 @@ __device__ __forceinline__ SeqTile find_tile(const int32_t *cu, int B, int n_tok
 }
 
 // ------------------------------------------------------ fp32 attention tile ----
-// FT_ROWS query rows against FT_KEYS keys at a time on the CUDA cores, one
-// pass over the keys with each row's running maximum and sum.  256 threads:
-// thread (ty, tx) of a 16 x 16 grid has rows ty*4..+3 and keys tx + 16*j of
-// the scores (4 x 4 fp32 accumulators), then the same rows and D/16 columns of
-// the output.  Products and sums are fp32: the operands and results of this
-// path are fp32 and a 16-bit product would lose them.
-constexpr int FT_ROWS = 64, FT_KEYS = 64, FT_THREADS = 256;
+// 16*R query rows against FT_KEYS keys at a time on the CUDA cores, one pass over
+// the keys with each row's running maximum and sum.  256 threads: thread (ty, tx)
+// of a 16 x 16 grid has rows ty*R..+R-1 and keys tx + 16*j of the scores, then
+// the same rows and D/16 columns of the output.  Products and sums are fp32: the
+// operands and results of this path are fp32 and a 16-bit product would lose
+// them.  R = 4 loads each operand from shared memory for four products; R = 2
+// cuts the work finer, for calls that would leave most SMs idle (small_ftiles).
+constexpr int FT_KEYS = 64, FT_THREADS = 256;
 
-template <int D>
+// Whether a call takes tiles of 32 rows: when its tiles of 64 would not give two
+// CTAs to each of the 148 SMs.
+inline bool small_ftiles(int64_t tiles64) { return tiles64 < 296; }
+
+template <int D, int R>
 struct FTile {
-    float q[FT_ROWS][D + 4];
+    float q[16 * R][D + 4];
     float k[FT_KEYS][D + 4];
     float v[FT_KEYS][D];
-    float p[FT_ROWS][FT_KEYS + 4];
+    float p[16 * R][FT_KEYS + 4];
 };
 
-template <int D>
+template <int D, int R>
 struct FState {
-    float o[4][D / 16];  // columns tx*4 + 64*j + e
-    float m[4], l[4];
+    float o[R][D / 16];  // columns tx*4 + 64*j + e
+    float m[R], l[R];
     __device__ __forceinline__ void init() {
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
+        for (int i = 0; i < R; i++) {
             m[i] = -INFINITY;
             l[i] = 0.f;
 #pragma unroll
@@ -110,24 +137,24 @@ struct FState {
 // only asked when `any_mask`.  `odd`: some value of v is infinite or NaN, and
 // left-out pairs must not touch it (0 * NaN is NaN), so they are marked by a
 // negative weight and skipped.  The caller synchronises before and after.
-template <int D, class Mask>
-__device__ __forceinline__ void ftile_step(FTile<D> &t, FState<D> &st, float qscale, bool any_mask, bool odd,
+template <int D, int R, class Mask>
+__device__ __forceinline__ void ftile_step(FTile<D, R> &t, FState<D, R> &st, float qscale, bool any_mask, bool odd,
                                            Mask masked) {
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-    float s[4][4];
+    float s[R][4];
 #pragma unroll
-    for (int i = 0; i < 4; i++)
+    for (int i = 0; i < R; i++)
 #pragma unroll
         for (int j = 0; j < 4; j++) s[i][j] = 0.f;
 #pragma unroll 4
     for (int d = 0; d < D; d += 4) {
-        float4 a[4], b[4];
+        float4 a[R], b[4];
 #pragma unroll
-        for (int i = 0; i < 4; i++) a[i] = *reinterpret_cast<const float4 *>(&t.q[ty * 4 + i][d]);
+        for (int i = 0; i < R; i++) a[i] = *reinterpret_cast<const float4 *>(&t.q[ty * R + i][d]);
 #pragma unroll
         for (int j = 0; j < 4; j++) b[j] = *reinterpret_cast<const float4 *>(&t.k[tx + 16 * j][d]);
 #pragma unroll
-        for (int i = 0; i < 4; i++)
+        for (int i = 0; i < R; i++)
 #pragma unroll
             for (int j = 0; j < 4; j++) {
                 s[i][j] = fmaf(a[i].x, b[j].x, s[i][j]);
@@ -137,13 +164,13 @@ __device__ __forceinline__ void ftile_step(FTile<D> &t, FState<D> &st, float qsc
             }
     }
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
+    for (int i = 0; i < R; i++) {
         uint32_t out = 0;
         float mx = -INFINITY;
 #pragma unroll
         for (int j = 0; j < 4; j++) {
             s[i][j] *= qscale;
-            if (any_mask && masked(ty * 4 + i, tx + 16 * j)) {
+            if (any_mask && masked(ty * R + i, tx + 16 * j)) {
                 out |= 1u << j;
                 s[i][j] = -INFINITY;
             }
@@ -160,7 +187,7 @@ __device__ __forceinline__ void ftile_step(FTile<D> &t, FState<D> &st, float qsc
             const bool gone = (out >> j) & 1u;
             const float p = gone ? 0.f : exp2f(s[i][j] - ms);
             sum += p;
-            t.p[ty * 4 + i][tx + 16 * j] = gone ? -1.f : p;
+            t.p[ty * R + i][tx + 16 * j] = gone ? -1.f : p;
         }
 #pragma unroll
         for (int o = 8; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
@@ -171,16 +198,16 @@ __device__ __forceinline__ void ftile_step(FTile<D> &t, FState<D> &st, float qsc
     }
     __syncwarp();  // a row's weights are written and read by the same half warp
     for (int n = 0; n < FT_KEYS; n += 4) {
-        float4 w[4];
+        float4 w[R];
 #pragma unroll
-        for (int i = 0; i < 4; i++) w[i] = *reinterpret_cast<const float4 *>(&t.p[ty * 4 + i][n]);
+        for (int i = 0; i < R; i++) w[i] = *reinterpret_cast<const float4 *>(&t.p[ty * R + i][n]);
 #pragma unroll
         for (int e = 0; e < 4; e++) {
             float4 v[D / 64];
 #pragma unroll
             for (int j = 0; j < D / 64; j++) v[j] = *reinterpret_cast<const float4 *>(&t.v[n + e][tx * 4 + 64 * j]);
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
+            for (int i = 0; i < R; i++) {
                 float p = e == 0 ? w[i].x : e == 1 ? w[i].y : e == 2 ? w[i].z : w[i].w;
                 if (p < 0.f) {
                     if (odd) continue;

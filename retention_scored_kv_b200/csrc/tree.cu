@@ -13,38 +13,39 @@ namespace {
 // What key a row of a key tile is.
 constexpr int32_t KEY_CACHE = -1, KEY_NONE = -2;  // >= 0: drafted token
 
-// One CTA per (head, 64 rows, part of the keys).  The keys of a head are its
+// One CTA per (head, 16*R rows, part of the keys).  The keys of a head are its
 // cache pages and then its drafted tokens in groups of 16; a tile of 64 is four
 // of either.  Parts of one (head, rows) meet through records in the workspace:
 // the last to arrive joins them in ascending order, so the result does not
 // depend on which one that is.
-template <int D>
+template <int D, int R>
 __global__ void __launch_bounds__(FT_THREADS) tree_ffma_kernel(const TreeArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];
-    FTile<D> &t = *reinterpret_cast<FTile<D> *>(smem);
-    int32_t *s_cu = reinterpret_cast<int32_t *>(smem + sizeof(FTile<D>));
+    FTile<D, R> &t = *reinterpret_cast<FTile<D, R> *>(smem);
+    int32_t *s_cu = reinterpret_cast<int32_t *>(smem + sizeof(FTile<D, R>));
+    constexpr int ROWS = 16 * R;
     __shared__ unsigned long long s_mask[64];
     __shared__ int32_t s_key[FT_KEYS];
     __shared__ const void *s_k[FT_KEYS], *s_v[FT_KEYS];
     __shared__ int s_last;
     if (!load_offsets(a.cu, a.B, a.n_tokens, a.max_nodes, s_cu, a.status)) return;
     const int part = blockIdx.x % a.parts, item = blockIdx.x / a.parts;
-    const int c = item / a.row_tiles, r0 = item % a.row_tiles * FT_ROWS;
+    const int c = item / a.row_tiles, r0 = item % a.row_tiles * ROWS;
     const int b = c / a.LH, lh = c % a.LH, G = a.G;
-    const int t0 = s_cu[b], nodes = s_cu[b + 1] - t0, R = nodes * G;
-    if (r0 >= R) return;
+    const int t0 = s_cu[b], nodes = s_cu[b + 1] - t0, rows = nodes * G;
+    if (r0 >= rows) return;
     const int m = clamp_len(__ldg(a.len + c), a.max_pages, a.status);
     const int np = (m + PAGE - 1) / PAGE, tiles = (np + (nodes + PAGE - 1) / PAGE + 3) / 4;
     if (threadIdx.x < nodes) s_mask[threadIdx.x] = __ldg(a.mask + t0 + threadIdx.x);
     constexpr int V4 = D / 4;
     const float *q = static_cast<const float *>(a.q);
-    for (int i = threadIdx.x; i < FT_ROWS * V4; i += FT_THREADS) {
+    for (int i = threadIdx.x; i < ROWS * V4; i += FT_THREADS) {
         const int r = r0 + i / V4, d = i % V4 * 4;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r < R) x = ld4(q + ((int64_t)(t0 + r / G) * a.LH * G + lh * G + r % G) * D + d);
+        if (r < rows) x = ld4(q + ((int64_t)(t0 + r / G) * a.LH * G + lh * G + r % G) * D + d);
         *reinterpret_cast<float4 *>(&t.q[i / V4][d]) = x;
     }
-    FState<D> st;
+    FState<D, R> st;
     st.init();
     const int last = (int)((int64_t)tiles * (part + 1) / a.parts);
     for (int j0 = (int)((int64_t)tiles * part / a.parts); j0 < last; j0++) {
@@ -79,19 +80,24 @@ __global__ void __launch_bounds__(FT_THREADS) tree_ffma_kernel(const TreeArgs a)
         }
         some = __syncthreads_or(some);
         int odd = 0;
-        for (int i = threadIdx.x; i < FT_KEYS * V4; i += FT_THREADS) {
-            const int r = i / V4, d = i % V4 * 4;
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-            if (s_k[r]) {
-                x = ld4(static_cast<const float *>(s_k[r]) + d);
-                y = ld4(static_cast<const float *>(s_v[r]) + d);
-                odd |= odd4(y);
-            }
-            *reinterpret_cast<float4 *>(&t.k[r][d]) = x;
-            *reinterpret_cast<float4 *>(&t.v[r][d]) = y;
+        constexpr int N = FT_KEYS * V4 / FT_THREADS;
+        float4 kr[N], vr[N];
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            const int e = i * FT_THREADS + threadIdx.x, r = e / V4, d = e % V4 * 4;
+            const bool in = s_k[r] != nullptr;
+            kr[i] = in ? ld4(static_cast<const float *>(s_k[r]) + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+            vr[i] = in ? ld4(static_cast<const float *>(s_v[r]) + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            const int e = i * FT_THREADS + threadIdx.x, r = e / V4, d = e % V4 * 4;
+            odd |= odd4(vr[i]);
+            *reinterpret_cast<float4 *>(&t.k[r][d]) = kr[i];
+            *reinterpret_cast<float4 *>(&t.v[r][d]) = vr[i];
         }
         odd = __syncthreads_or(odd);
-        ftile_step<D>(t, st, a.qscale, some != 0, odd != 0, [&](int row, int key) {
+        ftile_step<D, R>(t, st, a.qscale, some != 0, odd != 0, [&](int row, int key) {
             const int32_t kind = s_key[key];
             if (kind == KEY_CACHE) return false;
             const int node = (r0 + row) / G;
@@ -99,19 +105,19 @@ __global__ void __launch_bounds__(FT_THREADS) tree_ffma_kernel(const TreeArgs a)
         });
     }
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-    constexpr int REC = FT_ROWS * (D + 2);  // per part: output sums, then maxima and sums
+    constexpr int REC = ROWS * (D + 2);  // per part: output sums, then maxima and sums
     if (a.parts > 1) {
         float *rec = a.rec + ((int64_t)item * a.parts + part) * REC;
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const int r = ty * 4 + i;
+        for (int i = 0; i < R; i++) {
+            const int r = ty * R + i;
 #pragma unroll
             for (int j = 0; j < D / 64; j++)
                 st4(rec + r * D + tx * 4 + 64 * j, make_float4(st.o[i][4 * j], st.o[i][4 * j + 1], st.o[i][4 * j + 2],
                                                                st.o[i][4 * j + 3]));
             if (tx == 0) {
-                rec[FT_ROWS * D + r] = st.m[i];
-                rec[FT_ROWS * D + FT_ROWS + r] = st.l[i];
+                rec[ROWS * D + r] = st.m[i];
+                rec[ROWS * D + ROWS + r] = st.l[i];
             }
         }
         __threadfence();
@@ -125,9 +131,9 @@ __global__ void __launch_bounds__(FT_THREADS) tree_ffma_kernel(const TreeArgs a)
         for (int p = 0; p < a.parts; p++) {
             const float *rp = a.rec + ((int64_t)item * a.parts + p) * REC;
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const int r = ty * 4 + i;
-                const float mp = __ldcg(rp + FT_ROWS * D + r), lp = __ldcg(rp + FT_ROWS * D + FT_ROWS + r);
+            for (int i = 0; i < R; i++) {
+                const int r = ty * R + i;
+                const float mp = __ldcg(rp + ROWS * D + r), lp = __ldcg(rp + ROWS * D + ROWS + r);
                 const float mn = fmaxf(st.m[i], mp), ms = mn == -INFINITY ? 0.f : mn;
                 const float f = exp2f(st.m[i] - ms), g = exp2f(mp - ms);
                 st.m[i] = mn;
@@ -144,9 +150,9 @@ __global__ void __launch_bounds__(FT_THREADS) tree_ffma_kernel(const TreeArgs a)
         }
     }
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const int r = r0 + ty * 4 + i;
-        if (r >= R) continue;
+    for (int i = 0; i < R; i++) {
+        const int r = r0 + ty * R + i;
+        if (r >= rows) continue;
         const int64_t at = (int64_t)(t0 + r / G) * a.LH * G + lh * G + r % G;
         float *o = static_cast<float *>(a.out) + at * D;
         const bool none = st.m[i] == -INFINITY && st.l[i] == 0.f;
@@ -159,22 +165,21 @@ __global__ void __launch_bounds__(FT_THREADS) tree_ffma_kernel(const TreeArgs a)
     }
 }
 
-template <int D>
+template <int D, int R>
 cudaError_t launch_ffma(const TreeArgs &a, cudaStream_t s) {
-    const size_t smem = sizeof(FTile<D>) + (size_t)(a.B + 1) * 4;
-    cudaError_t e = cudaFuncSetAttribute(tree_ffma_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem);
+    const size_t smem = sizeof(FTile<D, R>) + (size_t)(a.B + 1) * 4;
+    cudaError_t e = cudaFuncSetAttribute(tree_ffma_kernel<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     const int64_t ctas = (int64_t)a.C * a.row_tiles * a.parts;
     if (ctas >= (1ll << 31)) return cudaErrorNotSupported;
-    tree_ffma_kernel<D><<<(unsigned)ctas, FT_THREADS, smem, s>>>(a);
+    tree_ffma_kernel<D, R><<<(unsigned)ctas, FT_THREADS, smem, s>>>(a);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-// Parts of each (head, 64 rows): enough for two CTAs on each of the 148 SMs
-// when there are few of them, up to 16.
+// Parts of each (head, rows): enough for two CTAs on each of the 148 SMs when
+// there are few of them, up to 16.
 static int ffma_parts(int64_t items) {
     const int64_t p = (295 + items) / items;
     return (int)(p > 16 ? 16 : p);
@@ -190,18 +195,20 @@ TreeLayout tree_layout(int dtype, int D, int G, int64_t C, int max_nodes) {
         L.rec_floats = (size_t)TREE_CTAS * 2 * L.rec_tiles * 128 * (D + 2);
         return L;
     }
-    L.row_tiles = (max_nodes * G + FT_ROWS - 1) / FT_ROWS;
+    L.rows = small_ftiles(C * ((max_nodes * G + 63) / 64)) ? 32 : 64;
+    L.row_tiles = (max_nodes * G + L.rows - 1) / L.rows;
     const int64_t items = C * L.row_tiles;
     L.parts = ffma_parts(items);
     // as many tickets for every max_nodes: calls of different sizes share a
     // workspace, and a record of one must not land on another's (zeroed) tickets
-    L.head_bytes = (size_t)C * ((TREE_MAX_NODES * G + FT_ROWS - 1) / FT_ROWS) * 4;
-    L.rec_floats = L.parts > 1 ? (size_t)items * L.parts * FT_ROWS * (D + 2) : 0;
+    L.head_bytes = (size_t)C * ((TREE_MAX_NODES * G + 31) / 32) * 4;
+    L.rec_floats = L.parts > 1 ? (size_t)items * L.parts * L.rows * (D + 2) : 0;
     return L;
 }
 
 cudaError_t launch_tree(const TreeArgs &a, int D, cudaStream_t s) {
-    return D == 64 ? launch_ffma<64>(a, s) : launch_ffma<128>(a, s);
+    if (a.row_tile == 32) return D == 64 ? launch_ffma<64, 2>(a, s) : launch_ffma<128, 2>(a, s);
+    return D == 64 ? launch_ffma<64, 4>(a, s) : launch_ffma<128, 4>(a, s);
 }
 
 }  // namespace rkv

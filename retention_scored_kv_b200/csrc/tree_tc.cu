@@ -689,6 +689,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     __shared__ uint32_t scan[33];
     unsigned char *tiles = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     const int warp = threadIdx.x >> 5;
+    launch_dependents();
     if (threadIdx.x == 0) {
         for (int s = 0; s < ITEMS; s++) {
             mbar_init(&sh.w_full[s], 1);
@@ -775,6 +776,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
 // columns) those of the item whose first part CTA x had; one thread a row.
 template <int D>
 __global__ void __launch_bounds__(QR) tree_join_kernel(const TreeArgs a) {
+    wait_for_launcher();
     const int4 d = a.join[blockIdx.x];
     if (d.x < 0) return;
     const int c = d.x, node0 = d.y, last = d.z, tile = blockIdx.y, col = blockIdx.z * 32, row = threadIdx.x;
@@ -814,8 +816,7 @@ cudaError_t launch(const TreeArgs &a, const CUtensorMap &tq, const CUtensorMap &
     if (e != cudaSuccess) return e;
     tree_tc_kernel<D><<<TREE_CTAS, TC_THREADS, Cfg<D>::SMEM, s>>>(a, tq, tk, tv, dk, dv);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    tree_join_kernel<D><<<dim3(TREE_CTAS, a.rec_tiles, D / 32), QR, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_after(tree_join_kernel<D>, dim3(TREE_CTAS, a.rec_tiles, D / 32), QR, 0, s, a);
 }
 
 }  // namespace
