@@ -198,57 +198,58 @@ __device__ __forceinline__ bool softmax_tile(uint32_t ts, uint32_t to, bool firs
     return true;
 }
 
-// 16 bytes of V without their infinite and NaN values; true if there were any.
+// 16 bytes of V without their infinite and NaN values (exponent field all ones);
+// true if there were any.
 __device__ __forceinline__ bool drop_odd(uint4 &v) {
     uint32_t bad = 0, *p = reinterpret_cast<uint32_t *>(&v);
 #pragma unroll
     for (int e = 0; e < 4; e++) {
-        const uint32_t m = __vcmpeq2(p[e] & 0x7F807F80u, 0x7F807F80u);
+        // adding one to an all-ones field carries into the bit above it
+        const uint32_t m = ((p[e] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
         bad |= m;
-        p[e] &= ~m;
+        p[e] &= ~((m >> 15) * 0xFFFFu);
     }
     return bad != 0;
 }
 
-// 32 columns of a row of bf16 results.
-__device__ __forceinline__ void store32(__nv_bfloat16 *out, const float (&f)[32]) {
-#pragma unroll
-    for (int e = 0; e < 32; e += 8)
-        *reinterpret_cast<uint4 *>(out + e) =
-            make_uint4(pack_bf16(f[e], f[e + 1]), pack_bf16(f[e + 2], f[e + 3]), pack_bf16(f[e + 4], f[e + 5]),
-                       pack_bf16(f[e + 6], f[e + 7]));
-}
-
-// 32 columns of a warp's 32 rows of bf16 results, lane i's row at out + at (where
-// `here`): through shared memory, so that a store instruction writes 64 bytes of
-// 8 rows instead of 16 bytes of 32.  Pieces of a row are exchanged by (row / 2) mod
-// 4 against bank conflicts.  Whole warp.
-__device__ __forceinline__ void store_rows(uint4 *stage, __nv_bfloat16 *out, int64_t at, bool here, const float (&f)[32]) {
+// 16 columns of a warp's 32 rows of bf16 results, lane i's row at out + at (where
+// `here`): through shared memory, so that a store instruction writes 32 bytes of
+// 16 rows instead of 16 bytes of 32.  Whole warp.
+__device__ __forceinline__ void store_rows(uint4 *stage, __nv_bfloat16 *out, int64_t at, uint32_t rows, const float (&f)[16]) {
     const int lane = threadIdx.x & 31;
-    const uint32_t rows = __ballot_sync(0xFFFFFFFFu, here);
 #pragma unroll
-    for (int e = 0; e < 4; e++)
-        stage[lane * 4 + (e ^ (lane >> 1 & 3))] =
+    for (int e = 0; e < 2; e++)  // a row's two pieces change places in every second group of four rows: no bank conflicts
+        stage[lane * 2 + (e ^ (lane >> 2 & 1))] =
             make_uint4(pack_bf16(f[8 * e], f[8 * e + 1]), pack_bf16(f[8 * e + 2], f[8 * e + 3]),
                        pack_bf16(f[8 * e + 4], f[8 * e + 5]), pack_bf16(f[8 * e + 6], f[8 * e + 7]));
     __syncwarp();
 #pragma unroll
-    for (int r = 0; r < 4; r++) {
-        const int row = r * 8 + lane / 4;
+    for (int r = 0; r < 2; r++) {
+        const int row = r * 16 + lane / 2;
         const int64_t to = __shfl_sync(0xFFFFFFFFu, at, row);
-        const uint4 v = stage[row * 4 + ((lane & 3) ^ (row >> 1 & 3))];
-        if (rows >> row & 1) *reinterpret_cast<uint4 *>(out + to + (lane & 3) * 8) = v;
+        const uint4 v = stage[row * 2 + ((lane & 1) ^ (row >> 2 & 1))];
+        if (rows >> row & 1) *reinterpret_cast<uint4 *>(out + to + (lane & 1) * 8) = v;
     }
     __syncwarp();
 }
 
-// Add the infinite and NaN values among 32 columns of one row of V, which the
-// tensor core was not shown.
-__device__ __forceinline__ void add_odd(float (&o)[32], const __nv_bfloat16 *v) {
-#pragma unroll
-    for (int e = 0; e < 32; e++) {
-        const float f = __bfloat162float(v[e]);
-        if (!(fabsf(f) < INFINITY)) o[e] += f;
+// Add the infinite and NaN values of one row of V, which the tensor core was not
+// shown, to columns [lo, hi) of this lane's row of O (`sees`: the row attends it).
+// Whole warp; rare, and kept out of line.
+template <int D>
+static __device__ __noinline__ void add_odd(uint32_t to, const __nv_bfloat16 *v, bool sees, int lo = 0, int hi = D) {
+#pragma unroll 1
+    for (int c = lo; c < hi; c++) {
+        const float f = __bfloat162float(v[c]);
+        const bool odd = sees && !(fabsf(f) < INFINITY);
+        if (!__any_sync(0xFFFFFFFFu, odd)) continue;
+        uint32_t o;
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(o) : "r"(to + c));
+        asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(o)::"memory");
+        if (odd) o = __float_as_uint(__uint_as_float(o) + f);
+        __syncwarp();
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(to + c), "r"(o) : "memory");
+        tmem_wait_st();
     }
 }
 

@@ -41,7 +41,7 @@ struct Shared {
     uint64_t v_last[8], v_ready[8];        // a slot's V of the last key tiles: loaded, and mended (full is not used)
     uint64_t w_full[2], w_empty[2];        // pieces of work
     Work work[2];
-    uint4 stage[8][32 * 4];                // results of a warp's rows, 32 columns
+    uint4 stage[8][32 * 2];                // results of a warp's rows, 16 columns
     uint32_t tmem;
 };
 
@@ -298,25 +298,25 @@ __device__ void softmax_role(const Ctx<D> &x, const PromptArgs &a) {
             const int r = (2 * wk.blk + i) * QR + row;  // row of the sequence
             const int odd = *(volatile int *)&sh->work[w.slot].odd;
             const bool here = r < wk.n;
-            const float inv = m == -INFINITY ? NAN : 1.f / l;  // every score -inf: 0 / 0
+            const float inv = m == -INFINITY ? NAN : __fdividef(1.f, l);  // every score -inf: 0 / 0
             __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + (int64_t)wk.hq * D;
+            if (__any_sync(0xFFFFFFFFu, odd)) {
+                const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.v) + (int64_t)(wk.hq / (a.Hq / a.H)) * D;
+                for (int j = 2 * wk.blk * KR; j < min(wk.n, nk * KR); j++) add_odd<D>(to, v + (wk.t0 + j) * a.v_stride, j <= r);
+            }
+            const uint32_t rows = __ballot_sync(0xFFFFFFFFu, here);
+            const int64_t at = (wk.t0 + (int64_t)r) * a.out_stride;
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-                uint32_t o[32];
-                tmem_ld32(o, to + c);
-                tmem_wait_ld32(o);
-                float f[32];
+            for (int c = 0; c < D; c += 16) {
+                uint32_t o[16];
+                tmem_read16(o, to + c);
+                float f[16];
 #pragma unroll
-                for (int e = 0; e < 32; e++) f[e] = __uint_as_float(o[e]) * inv;
-                if (odd && here) {
-                    const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.v) + (int64_t)wk.t0 * a.v_stride +
-                                             (int64_t)(wk.hq / (a.Hq / a.H)) * D + c;
-                    for (int j = 2 * wk.blk * KR; j <= r; j++) add_odd(f, v + j * a.v_stride);
-                }
-                store_rows(sh->stage[threadIdx.x >> 5], out + c, (wk.t0 + (int64_t)r) * a.out_stride, here, f);
+                for (int e = 0; e < 16; e++) f[e] = __uint_as_float(o[e]) * inv;
+                store_rows(sh->stage[threadIdx.x >> 5], out + c, at, rows, f);
             }
             tc_fence_before();
-            if (here && a.lse) a.lse[(wk.t0 + (int64_t)r) * a.Hq + wk.hq] = (m * qscale + log2f(l)) * LN2;
+            if (here && a.lse) a.lse[(wk.t0 + (int64_t)r) * a.Hq + wk.hq] = (m * qscale + __log2f(l)) * LN2;
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh->o_free[i]);
         }

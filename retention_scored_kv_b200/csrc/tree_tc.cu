@@ -70,9 +70,10 @@ struct Shared {
     uint64_t m_full[4], m_empty[4]; // tiles to mend
     Item item[ITEMS];
     Tile tile[WORDS];
+    __align__(16) int32_t k_page[8], v_page[8];   // pages of the tile that is being issued
     uint32_t part[WORDS];           // some row of the tile does not count, or is of a drafted token
     Mend mend[4];
-    uint4 stage[8][32 * 4];         // results of a warp's rows, 32 columns: from a row a lane to whole lines
+    uint4 stage[8][32 * 2];         // results of a warp's rows, 16 columns: from a row a lane to whole sectors
     float2 ml[2][2][QR];            // one-tile items: maximum and sum of both warpgroups (by item, warpgroup)
     uint32_t tmem;
     int c0, p0;                     // first head of this CTA's range and the work before it
@@ -107,7 +108,7 @@ struct Head {
 // Start of CTA i's range when `total` is cut into n.
 __device__ __forceinline__ int cut(int total, int i, int n) { return (int)((int64_t)total * i / n); }
 // CTA whose range holds position x.
-__device__ __forceinline__ int cta_of(int total, int x, int n) {
+static __device__ __noinline__ int cta_of(int total, int x, int n) {
     int i = (int)((int64_t)x * n / total);
     while (cut(total, i + 1, n) <= x) i++;
     while (cut(total, i, n) > x) i--;
@@ -182,16 +183,30 @@ struct Groups {
     }
 };
 
-// One group of 16 rows: a page, or two blocks of 8 rows of the draft.
+// The eight groups of a key tile: pages of the pool, or (drafts) two blocks of 8
+// rows each of the drafted tokens; only those with their bit in live.  Whole
+// warp; one elected thread issues, with the operands in uniform registers.
 template <int D>
-__device__ __forceinline__ void load_group(unsigned char *dst, const CUtensorMap *pool, const CUtensorMap *draft_map, bool draft,
-                                           int32_t pg, int lh, uint64_t *bar) {
-    if (!draft) {
-        tma_load_4d(dst, pool, 0, 0, 0, pg * 2, bar);
-    } else {
-        tma_tile(dst, draft_map, 0, pg, lh * (D / 64), bar);
-        tma_tile(dst + Cfg<D>::BLOCK, draft_map, 0, pg + 8, lh * (D / 64), bar);
+static __device__ __noinline__ void issue_tile(unsigned char *dst, const CUtensorMap *pool, const CUtensorMap *draft_map,
+                                               const int32_t *pages, uint32_t live, uint32_t drafts, int lh, uint64_t *bar) {
+    using C = Cfg<D>;
+    if (elect_one()) {
+        mbar_arrive_expect_tx(bar, __popc(live) * C::GROUP);
+        int32_t pg[8];
+        *reinterpret_cast<int4 *>(pg) = *reinterpret_cast<const int4 *>(pages);
+        *reinterpret_cast<int4 *>(pg + 4) = *reinterpret_cast<const int4 *>(pages + 4);
+        const uint32_t paged = live & ~drafts;
+#pragma unroll
+        for (int g = 0; g < 8; g++)
+            if (paged >> g & 1) tma_load_4d(dst + g * C::GROUP, pool, 0, 0, 0, pg[g] * 2, bar);
+#pragma unroll 1
+        for (uint32_t left = live & drafts; left; left &= left - 1) {
+            const int g = __ffs(left) - 1, row = pages[g];
+            tma_tile(dst + g * C::GROUP, draft_map, 0, row, lh * (D / 64), bar);
+            tma_tile(dst + g * C::GROUP + C::BLOCK, draft_map, 0, row + 8, lh * (D / 64), bar);
+        }
     }
+    __syncwarp();
 }
 
 // The items of this CTA's range in order.
@@ -231,7 +246,8 @@ __device__ void load_role(const Ctx<D> &x, const TreeArgs &a, int n, const CUten
     Head h(a, at.c, a.status);
     Item it;
     // the next item from `at` on; raw: the head after at.c is read already
-    auto seek = [&](bool raw, int32_t r0, int32_t r1, int32_t rn) {
+    int32_t r0 = 0, r1 = 0, rn = 0;
+    auto seek = [&](bool raw) {
         for (;;) {
             if (at.k < h.items && at.pre < sh->end) {
                 if (at.item(a, sh, h, it)) return true;
@@ -245,69 +261,83 @@ __device__ void load_role(const Ctx<D> &x, const TreeArgs &a, int n, const CUten
             raw = false;
         }
     };
-    Groups groups, ahead;
-    bool ok = true, have = seek(false, 0, 0, 0), posted = false;
-    if (have) ahead.start(a, it);
+    bool posted = false;
     auto post = [&] {
         if (lane == 0) {
             sh->item[w.slot] = it;
             mbar_arrive(&sh->w_full[w.slot]);
             if (it.rec >= 0 && it.lo == 0)  // the item's first part: it describes the item to the join
-                a.join[blockIdx.x] =
-                    make_int4(it.c, it.node0, cta_of(sh->total, at.pre + COST + h.tiles - 1, n), 0);
+                a.join[blockIdx.x] = make_int4(it.c, it.node0, cta_of(sh->total, at.pre + COST + h.tiles - 1, n), 0);
         }
         w.next(ITEMS);
         posted = true;
     };
-    while (ok && have) {
-        if (!posted) {
-            if (!(ok = warp_wait(&sh->w_empty[w.slot], w.turn ^ 1u, a.status, 0x440))) break;
-            post();
+    Groups groups, ahead;
+    Item now{};
+    bool ok = true;
+    // Turn by turn: the tiles of the item posted before, behind the first of them
+    // the search for the next one; the first turn only searches.
+#pragma unroll 1
+    for (bool begin = true, have = true; ok && have; begin = false) {
+        if (!begin) {
+            if (!posted && !(ok = warp_wait(&sh->w_empty[w.slot], w.turn ^ 1u, a.status, 0x440))) break;
+            if (!posted) post();
+            posted = false;
+            now = it;
+            groups = ahead;
+            // raw lengths and offsets of the next head, used after the first tile
+            const int c2 = min(at.c + 1, a.C - 1), b2 = c2 / a.LH;
+            r0 = __ldg(a.cu + b2);
+            r1 = __ldg(a.cu + b2 + 1);
+            rn = __ldg(a.len + c2);
         }
-        posted = false;
-        const Item now = it;
         const int lh = now.c % a.LH;
-        groups = ahead;
-        // raw lengths and offsets of the next head, used after the first tile
-        const int c2 = min(at.c + 1, a.C - 1), b2 = c2 / a.LH;
-        const int32_t r0 = __ldg(a.cu + b2), r1 = __ldg(a.cu + b2 + 1), rn = __ldg(a.len + c2);
-        for (int j = now.lo; j < now.hi; j++, tile_no++) {
-            int32_t pg;
-            uint32_t wd;
-            bool draft;
-            groups.tile(j, j - now.lo, a.n_pages, a.status, pg, wd, draft);
-            const uint32_t live = __ballot_sync(0xFFFFFFFFu, wd != 0);
-            const uint32_t part = __ballot_sync(0xFFFFFFFFu, lane < 8 && (wd != 0xFFFFu || draft));
-            if (!(ok = warp_wait(&sh->k_empty[kr.slot], kr.turn ^ 1u, a.status, 0x442))) break;
-            if (lane < 8) sh->tile[tile_no % WORDS].word[lane] = (uint16_t)wd;
-            if (lane == 0) sh->part[tile_no % WORDS] = part;
-            __syncwarp();
-            uint64_t *bar = &sh->k_full[kr.slot];
-            if (lane == 0) mbar_arrive_expect_tx(bar, __popc(live) * C::GROUP);
-            __syncwarp();
-            if (wd) load_group<D>(x.k_slot(kr.slot) + lane * C::GROUP, tk, dk, draft, pg, lh, bar);
-            kr.next(C::KS);
-            if (j > now.lo) continue;
-            // the item's one or two query tiles, behind its first key tile: their
-            // slots are free only when the products of the item before are done
-            for (int i = 0; ok && i < (now.rows[1] ? 2 : 1); i++) {
-                if (!(ok = warp_wait(&sh->q_empty[qr.slot], qr.turn ^ 1u, a.status, 0x441))) break;
-                if (lane == 0) mbar_arrive_expect_tx(&sh->q_full[qr.slot], (uint32_t)(a.nt * a.G * D * 2));
+#pragma unroll 1
+        for (int j = now.lo; j < now.hi || begin; j++, tile_no++) {
+            if (!begin) {
+                int32_t pg;
+                uint32_t wd;
+                bool draft;
+                groups.tile(j, j - now.lo, a.n_pages, a.status, pg, wd, draft);
+                const uint32_t live = __ballot_sync(0xFFFFFFFFu, wd != 0);
+                const uint32_t part = __ballot_sync(0xFFFFFFFFu, lane < 8 && (wd != 0xFFFFu || draft));
+                const uint32_t drafts = __ballot_sync(0xFFFFFFFFu, wd != 0 && draft);
+                if (!(ok = warp_wait(&sh->k_empty[kr.slot], kr.turn ^ 1u, a.status, 0x442))) break;
+                if (lane < 8) {
+                    sh->tile[tile_no % WORDS].word[lane] = (uint16_t)wd;
+                    sh->k_page[lane] = pg;
+                }
+                if (lane == 0) sh->part[tile_no % WORDS] = part;
                 __syncwarp();
-                if (lane < D / 64)
-                    tma_tile(x.q + qr.slot * C::TILE + lane * C::PLANE, tq, lane * 64, lh * a.G, now.t0 + now.node0 + i * a.nt,
-                             &sh->q_full[qr.slot]);
-                qr.next(2);
+                issue_tile<D>(x.k_slot(kr.slot), tk, dk, sh->k_page, live, drafts, lh, &sh->k_full[kr.slot]);
+                kr.next(C::KS);
+                if (j > now.lo) continue;
+                // the item's one or two query tiles, behind its first key tile: their
+                // slots are free only when the products of the item before are done
+#pragma unroll 1
+                for (int i = 0; ok && i < (now.rows[1] ? 2 : 1); i++) {
+                    if (!(ok = warp_wait(&sh->q_empty[qr.slot], qr.turn ^ 1u, a.status, 0x441))) break;
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(&sh->q_full[qr.slot], (uint32_t)(a.nt * a.G * D * 2));
+#pragma unroll
+                        for (int p = 0; p < D / 64; p++)
+                            tma_tile(x.q + qr.slot * C::TILE + p * C::PLANE, tq, p * 64, lh * a.G,
+                                     now.t0 + now.node0 + i * a.nt, &sh->q_full[qr.slot]);
+                    }
+                    __syncwarp();
+                    qr.next(2);
+                }
+                if (!ok) break;
+                at.k++;
+                at.pre += h.tiles + COST;
             }
-            if (!ok) break;
             // the next item
-            at.k++;
-            at.pre += h.tiles + COST;
-            have = seek(true, r0, r1, rn);
+            have = seek(!begin);
             if (have) {
                 ahead.start(a, it);
-                if (warp_test(&sh->w_empty[w.slot], w.turn ^ 1u)) post();
+                if (!begin && warp_test(&sh->w_empty[w.slot], w.turn ^ 1u)) post();
             }
+            if (begin) break;
         }
     }
     // the end: an item without rows
@@ -336,6 +366,7 @@ __device__ void value_role(const Ctx<D> &x, const TreeArgs &a, const CUtensorMap
         Ring next = w;
         next.next(ITEMS);
         const int lh = it.c % a.LH;
+#pragma unroll 1
         for (int j = it.lo; j < it.hi; j++) {
             int32_t pg;
             uint32_t wd;
@@ -359,9 +390,9 @@ __device__ void value_role(const Ctx<D> &x, const TreeArgs &a, const CUtensorMap
                 if (lane == 0) mbar_arrive(&sh->m_full[mr.slot]);
                 mr.next(4);
             }
-            if (lane == 0) mbar_arrive_expect_tx(bar, __popc(live) * C::GROUP);
+            if (lane < 8) sh->v_page[lane] = pg;
             __syncwarp();
-            if (wd) load_group<D>(x.v_slot(vr.slot) + lane * C::GROUP, tv, dv, draft, pg, lh, bar);
+            issue_tile<D>(x.v_slot(vr.slot), tv, dv, sh->v_page, live, drafts, lh, bar);
             vr.next(C::VS);
             if (!early && warp_test(&sh->w_full[next.slot], next.turn)) {
                 // the next item is there: its first pages
@@ -500,24 +531,21 @@ __device__ void mend_role(const Ctx<D> &x) {
             return (row >> 3) * (C::BLOCK / 16) + (row & 7) * 8;
         };
         bool odd = false;
+#pragma unroll 1
         for (int g = 0; g < 8; g++) {
             const uint32_t word = md.word[g];
             uint4 *group = reinterpret_cast<uint4 *>(x.v_slot(md.slot) + g * C::GROUP) + piece;
-            if (md.draft >> g & 1) {
-                uint4 v[16 / ROWS];
-#pragma unroll
-                for (int r = 0; r < 16 / ROWS; r++) v[r] = group[at(r)];
-#pragma unroll
-                for (int r = 0; r < 16 / ROWS; r++) {
-                    const uint32_t keep = 0u - (word >> (r * ROWS + lane / PIECES) & 1u);
-                    v[r] = make_uint4(v[r].x & keep, v[r].y & keep, v[r].z & keep, v[r].w & keep);
-                    odd |= drop_odd(v[r]);
-                    group[at(r)] = v[r];
+            const bool draft = md.draft >> g & 1;
+            if (word == 0xFFFFu && !draft) continue;
+#pragma unroll 2
+            for (int r = 0; r < 16 / ROWS; r++) {
+                uint4 *p = group + at(r), v = make_uint4(0, 0, 0, 0);
+                const bool in = word >> (r * ROWS + lane / PIECES) & 1u;
+                if (draft && in) {
+                    v = *p;
+                    odd |= drop_odd(v);
                 }
-            } else if (word != 0xFFFFu) {
-#pragma unroll
-                for (int r = 0; r < 16 / ROWS; r++)
-                    if (!(word >> (r * ROWS + lane / PIECES) & 1u)) group[at(r)] = make_uint4(0, 0, 0, 0);
+                if (draft || !in) *p = v;
             }
         }
         if (odd) atomicOr(&sh->item[md.item].odd, 1);
@@ -554,6 +582,7 @@ __device__ void softmax_role(const Ctx<D> &x, const TreeArgs &a) {
         if (row < rows) mask = __ldg(a.mask + it.t0 + node);
         float m = -INFINITY, l = 0.f;
         int mine = 0;
+#pragma unroll 1
         for (int j = two ? 0 : i; j < n; j += two ? 1 : 2, mine++) {
             if (!x.wait(&sh->s_full[i], s_turn, 0x471)) return;
             s_turn ^= 1u;
@@ -624,48 +653,45 @@ __device__ void softmax_role(const Ctx<D> &x, const TreeArgs &a) {
             const bool none = m == -INFINITY;
             const int lh = it.c % a.LH;
             const int64_t at = (int64_t)(it.t0 + node) * a.LH * a.G + (int64_t)lh * a.G + row % a.G;  // row of q and out
-            const float inv = it.rec >= 0 ? 1.f : none ? 0.f : 1.f / l;
+            const float inv = it.rec >= 0 ? 1.f : none ? 0.f : __fdividef(1.f, l);
             float *rec = nullptr;
             if (it.rec >= 0) rec = a.rec + ((int64_t)it.rec * a.rec_tiles + (two ? i : 0)) * (QR * (D + 2)) + row;
+            if (__any_sync(0xFFFFFFFFu, odd)) {
+                scale0 = fmaxf(scale0, 0x1p-100f);  // infinite values pass, finite ones vanish as with 0
+                for (int d = 0; d < it.nodes; d++)
+                    add_odd<D>(two ? to : o0, static_cast<const __nv_bfloat16 *>(a.v_draft) + ((int64_t)(it.t0 + d) * a.LH + lh) * D,
+                               here && (mask >> d & 1ull), c_lo, c_hi);
+            }
+            const uint32_t rows_here = __ballot_sync(0xFFFFFFFFu, here);
+            const uint32_t first = two ? to : o0;
+            scale0 *= inv;
+            scale1 *= inv;
 #pragma unroll 1
-            for (int c = c_lo; c < c_hi; c += 32) {
-                float f[32];
-                {
-                    uint32_t o[32];
-                    tmem_ld32(o, (two ? to : o0) + c);
-                    tmem_wait_ld32(o);
+            for (int c = c_lo; c < c_hi; c += 16) {
+                uint32_t o[16];
+                float f[16];
+                tmem_read16(o, first + c);
 #pragma unroll
-                    for (int e = 0; e < 32; e++) f[e] = __uint_as_float(o[e]) * scale0;
-                }
+                for (int e = 0; e < 16; e++) f[e] = __uint_as_float(o[e]) * scale0;
                 if (!two && n > 1) {
-                    uint32_t o[32];
-                    tmem_ld32(o, o0 + D + c);
-                    tmem_wait_ld32(o);
+                    tmem_read16(o, o0 + D + c);
 #pragma unroll
-                    for (int e = 0; e < 32; e++) f[e] = fmaf(__uint_as_float(o[e]), scale1, f[e]);
+                    for (int e = 0; e < 16; e++) f[e] = fmaf(__uint_as_float(o[e]), scale1, f[e]);
                 }
-                if (odd && here)
-                    for (int d = 0; d < it.nodes; d++)
-                        if (mask >> d & 1ull)
-                            add_odd(f, static_cast<const __nv_bfloat16 *>(a.v_draft) + ((int64_t)(it.t0 + d) * a.LH + lh) * D + c);
+                if (it.rec < 0) {
+                    store_rows(sh->stage[threadIdx.x >> 5], static_cast<__nv_bfloat16 *>(a.out) + c, at * D, rows_here, f);
+                } else if (here) {
 #pragma unroll
-                for (int e = 0; e < 32; e++) f[e] *= inv;
-                if (it.rec >= 0) {
-                    if (here) {
-#pragma unroll
-                        for (int e = 0; e < 32; e++) rec[(c + e) * QR] = f[e];
-                    }
-                    __syncwarp();
-                } else {
-                    store_rows(sh->stage[threadIdx.x >> 5], static_cast<__nv_bfloat16 *>(a.out) + c, at * D, here, f);
+                    for (int e = 0; e < 16; e++) rec[(c + e) * QR] = f[e];
                 }
+                __syncwarp();
             }
             if (here && c_lo == 0) {
                 if (rec) {
                     rec[D * QR] = m;
                     rec[(D + 1) * QR] = l;
                 } else if (a.lse) {
-                    a.lse[at] = none ? -INFINITY : (m * qscale + log2f(l)) * LN2;
+                    a.lse[at] = none ? -INFINITY : (m * qscale + __log2f(l)) * LN2;
                 }
             }
         }
@@ -805,7 +831,11 @@ __global__ void __launch_bounds__(QR) tree_join_kernel(const TreeArgs a) {
     const float inv = none ? 0.f : 1.f / l;
 #pragma unroll
     for (int e = 0; e < 32; e++) f[e] *= inv;
-    store32(static_cast<__nv_bfloat16 *>(a.out) + at * D + col, f);
+    uint4 *out = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + at * D + col);
+#pragma unroll
+    for (int e = 0; e < 4; e++)
+        out[e] = make_uint4(pack_bf16(f[8 * e], f[8 * e + 1]), pack_bf16(f[8 * e + 2], f[8 * e + 3]),
+                            pack_bf16(f[8 * e + 4], f[8 * e + 5]), pack_bf16(f[8 * e + 6], f[8 * e + 7]));
     if (a.lse && col == 0) a.lse[at] = none ? -INFINITY : (m * qscale + log2f(l)) * LN2;
 }
 
