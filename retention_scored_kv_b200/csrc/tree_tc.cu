@@ -15,9 +15,9 @@
 // end leaves its parts' unnormalised outputs, maxima and sums in the workspace,
 // and tree_join_kernel joins them in ascending order.
 //
-// Warps 0-7: softmax and results.  Warp 8: items, queries, K, keep words.  Warp
-// 9: issues the products.  Warp 10: V.  Warp 11: V of key tiles with rows that do
-// not count: those become zero (0 * NaN would reach every row), and infinite or NaN
+// Warps 0-7: softmax and results.  Warp 8: items, queries, K, and a record of
+// each key tile (pages, keep words) that the others follow.  Warp 9: issues the
+// products.  Warp 10: V.  Warp 11: V of key tiles with rows that do not count: those become zero (0 * NaN would reach every row), and infinite or NaN
 // values of drafted tokens too (not every row attends them; the results add them
 // for those that do).
 #include "attn_tc.cuh"
@@ -45,21 +45,22 @@ struct Cfg {
 __host__ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
 struct Item {
-    int c, t0, node0, nodes;  // head, first token of its sequence, first token of the item's, tokens of the sequence
-    int rows[2];              // rows of the query tiles (rows[1] = 0: one tile)
-    int lo, hi, np, len;      // key tiles of this part; cache pages and entries of the head
-    int rec;                  // -1: the item is whole; else the record of this part
-    int odd;                  // V of some drafted token held infinities or NaN
+    int c, lh, t0, node0, nodes;  // head (of all, of its sequence), first token of its sequence and of the item, tokens of the sequence
+    int rows[2];                  // rows of the query tiles (rows[1] = 0: one tile)
+    int lo, hi, np, len;          // key tiles of this part; cache pages and entries of the head
+    int rec;                      // -1: the item is whole; else the record of this part
+    int odd;                      // V of some drafted token held infinities or NaN
 };
 
+// A key tile.
 struct __align__(16) Tile {
-    uint16_t word[8];  // bit r: row r of group g counts
+    uint16_t word[8];             // bit r: row r of group g counts
+    int32_t page[8];              // page of the pool, or first row of the draft
+    uint32_t live, drafts;        // groups with a row that counts (END: no more tiles), and those of drafted tokens
+    uint32_t part;                // some row does not count, or is of a drafted token
+    uint32_t item_lh;             // slot of the item, and lh << 8
 };
-
-struct Mend {
-    int slot, item, draft;  // draft: bit g: group g is of drafted tokens
-    uint16_t word[8];
-};
+constexpr uint32_t END = 0xFFFFFFFFu;
 
 struct Shared {
     uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
@@ -67,12 +68,9 @@ struct Shared {
     uint64_t q_full[2], q_empty[2];
     uint64_t s_full[2], p_full[2][2], o_done[2], o_free, ml_full;  // p_full: by halves of the keys
     uint64_t w_full[ITEMS], w_empty[ITEMS]; // items
-    uint64_t m_full[4], m_empty[4]; // tiles to mend
+    uint64_t t_full[WORDS], t_empty[WORDS]; // tiles' records
     Item item[ITEMS];
     Tile tile[WORDS];
-    __align__(16) int32_t k_page[8], v_page[8];   // pages of the tile that is being issued
-    uint32_t part[WORDS];           // some row of the tile does not count, or is of a drafted token
-    Mend mend[4];
     uint4 stage[8][32 * 2];         // results of a warp's rows, 16 columns: from a row a lane to whole sectors
     float2 ml[2][2][QR];            // one-tile items: maximum and sum of both warpgroups (by item, warpgroup)
     uint32_t tmem;
@@ -116,7 +114,7 @@ static __device__ __noinline__ int cta_of(int total, int x, int n) {
 }
 
 // ------------------------------------------------- warps 8 and 10: loads ----
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int32_t *status, int site) {
+static __device__ __noinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int32_t *status, int site) {
     int good = 1;
     if ((threadIdx.x & 31) == 0) good = tc_wait(bar, parity, status, site);
     return __shfl_sync(0xFFFFFFFFu, good, 0) != 0;
@@ -209,92 +207,51 @@ static __device__ __noinline__ void issue_tile(unsigned char *dst, const CUtenso
     __syncwarp();
 }
 
-// The items of this CTA's range in order.
-struct Walk {
-    int c, k, pre;
-    __device__ bool item(const TreeArgs &a, const Shared *sh, const Head &h, Item &it) const {
-        it = Item{};
-        it.lo = max(0, min(h.tiles, sh->begin - pre - COST));
-        it.hi = max(0, min(h.tiles, sh->end - pre - COST));
-        it.c = c;
-        it.t0 = h.t0;
-        it.nodes = h.nodes;
-        it.np = h.np;
-        it.len = h.len;
-        it.node0 = k * 2 * a.nt;
-        const int left = h.nodes - it.node0;
-        it.rows[0] = min(left, a.nt) * a.G;
-        it.rows[1] = left > a.nt ? min(left - a.nt, a.nt) * a.G : 0;
-        it.rec = -1;
-        if (it.lo > 0 || it.hi < h.tiles) it.rec = 2 * (int)blockIdx.x + (it.lo == 0 ? 1 : 0);
-        return it.lo < it.hi;
-    }
-};
-
-// Warp 8: items, queries, K and the tiles' keep words.  An item's head, its first
-// pages and (where the ring has room) the item itself are read and handed on
-// while the item before it is loaded, so that short heads follow without a gap.
+// Warp 8.  An item's head, its first pages and (where the ring has room) the item
+// itself are read and handed on while the item before it is loaded, so that
+// short heads follow without a gap.
 template <int D>
 __device__ void load_role(const Ctx<D> &x, const TreeArgs &a, int n, const CUtensorMap *tq, const CUtensorMap *tk,
                           const CUtensorMap *dk) {
     using C = Cfg<D>;
     Shared *sh = x.sh;
-    const int lane = threadIdx.x & 31;
-    Ring kr, w, qr;
-    int tile_no = 0;
-    Walk at{sh->c0, 0, sh->p0};
-    Head h(a, at.c, a.status);
-    Item it;
-    // the next item from `at` on; raw: the head after at.c is read already
-    int32_t r0 = 0, r1 = 0, rn = 0;
-    auto seek = [&](bool raw) {
-        for (;;) {
-            if (at.k < h.items && at.pre < sh->end) {
-                if (at.item(a, sh, h, it)) return true;
-                at.k++;
-                at.pre += h.tiles + COST;
-                continue;
-            }
-            if (++at.c >= a.C || at.pre >= sh->end) return false;
-            at.k = 0;
-            h = raw ? Head(a, r0, r1, rn, a.status) : Head(a, at.c, a.status);
-            raw = false;
-        }
-    };
-    bool posted = false;
-    auto post = [&] {
-        if (lane == 0) {
-            sh->item[w.slot] = it;
-            mbar_arrive(&sh->w_full[w.slot]);
-            if (it.rec >= 0 && it.lo == 0)  // the item's first part: it describes the item to the join
-                a.join[blockIdx.x] = make_int4(it.c, it.node0, cta_of(sh->total, at.pre + COST + h.tiles - 1, n), 0);
-        }
-        w.next(ITEMS);
-        posted = true;
-    };
+    const int lane = threadIdx.x & 31, begin = sh->begin, end = sh->end;
+    Ring kr, w, qr, tr;
+    int c = sh->c0, lh = c % a.LH, b = c / a.LH, k = 0, pre = sh->p0;  // next head, item of it, work before that
+    int32_t r0 = __ldg(a.cu + b), r1 = __ldg(a.cu + b + 1), rn = __ldg(a.len + c);  // of head c
+    Head h(a, r0, r1, rn, a.status);
     Groups groups, ahead;
-    Item now{};
-    bool ok = true;
-    // Turn by turn: the tiles of the item posted before, behind the first of them
-    // the search for the next one; the first turn only searches.
+    Item it{}, now{};
+    bool posted = false;
+    auto wait = [&](uint64_t *bar, uint32_t parity, int site) { return warp_wait(bar, parity, a.status, site); };
+    // Turn by turn: the tiles of the item found before and, behind the first of
+    // them, the search for the next one; the first turn only searches.
 #pragma unroll 1
-    for (bool begin = true, have = true; ok && have; begin = false) {
-        if (!begin) {
-            if (!posted && !(ok = warp_wait(&sh->w_empty[w.slot], w.turn ^ 1u, a.status, 0x440))) break;
-            if (!posted) post();
-            posted = false;
+    for (bool first = true, have = true; have; first = false) {
+        if (!first) {
+            if (!posted) {
+                if (!wait(&sh->w_empty[w.slot], w.turn ^ 1u, 0x440)) return;
+                posted = true;
+                if (lane == 0) {
+                    sh->item[w.slot] = it;
+                    mbar_arrive(&sh->w_full[w.slot]);
+                }
+                w.next(ITEMS);
+            }
             now = it;
             groups = ahead;
-            // raw lengths and offsets of the next head, used after the first tile
-            const int c2 = min(at.c + 1, a.C - 1), b2 = c2 / a.LH;
-            r0 = __ldg(a.cu + b2);
-            r1 = __ldg(a.cu + b2 + 1);
-            rn = __ldg(a.len + c2);
+            posted = false;
         }
-        const int lh = now.c % a.LH;
+        // the slot of the item that was posted last
+        const uint32_t item_lh = (uint32_t)((w.slot + ITEMS - 1) % ITEMS) | (uint32_t)now.lh << 8;
+        // raw lengths and offsets of the head after h, used after the first tile
+        const int lh2 = lh + 1 == a.LH ? 0 : lh + 1, b2 = min(lh2 ? b : b + 1, a.B - 1);
+        r0 = __ldg(a.cu + b2);
+        r1 = __ldg(a.cu + b2 + 1);
+        rn = __ldg(a.len + min(c + 1, a.C - 1));
 #pragma unroll 1
-        for (int j = now.lo; j < now.hi || begin; j++, tile_no++) {
-            if (!begin) {
+        for (int j = now.lo; j < now.hi || first; j++) {
+            if (!first) {
                 int32_t pg;
                 uint32_t wd;
                 bool draft;
@@ -302,114 +259,122 @@ __device__ void load_role(const Ctx<D> &x, const TreeArgs &a, int n, const CUten
                 const uint32_t live = __ballot_sync(0xFFFFFFFFu, wd != 0);
                 const uint32_t part = __ballot_sync(0xFFFFFFFFu, lane < 8 && (wd != 0xFFFFu || draft));
                 const uint32_t drafts = __ballot_sync(0xFFFFFFFFu, wd != 0 && draft);
-                if (!(ok = warp_wait(&sh->k_empty[kr.slot], kr.turn ^ 1u, a.status, 0x442))) break;
+                if (!wait(&sh->t_empty[tr.slot], tr.turn ^ 1u, 0x443)) return;
+                Tile *t = &sh->tile[tr.slot];
                 if (lane < 8) {
-                    sh->tile[tile_no % WORDS].word[lane] = (uint16_t)wd;
-                    sh->k_page[lane] = pg;
+                    t->word[lane] = (uint16_t)wd;
+                    t->page[lane] = pg;
                 }
-                if (lane == 0) sh->part[tile_no % WORDS] = part;
+                if (lane == 0) {
+                    t->live = live;
+                    t->drafts = drafts;
+                    t->part = part;
+                    t->item_lh = item_lh;
+                }
                 __syncwarp();
-                issue_tile<D>(x.k_slot(kr.slot), tk, dk, sh->k_page, live, drafts, lh, &sh->k_full[kr.slot]);
+                if (lane == 0) mbar_arrive(&sh->t_full[tr.slot]);
+                tr.next(WORDS);
+                if (!wait(&sh->k_empty[kr.slot], kr.turn ^ 1u, 0x442)) return;
+                issue_tile<D>(x.k_slot(kr.slot), tk, dk, t->page, live, drafts, now.lh, &sh->k_full[kr.slot]);
                 kr.next(C::KS);
                 if (j > now.lo) continue;
                 // the item's one or two query tiles, behind its first key tile: their
                 // slots are free only when the products of the item before are done
 #pragma unroll 1
-                for (int i = 0; ok && i < (now.rows[1] ? 2 : 1); i++) {
-                    if (!(ok = warp_wait(&sh->q_empty[qr.slot], qr.turn ^ 1u, a.status, 0x441))) break;
+                for (int i = 0; i < (now.rows[1] ? 2 : 1); i++) {
+                    if (!wait(&sh->q_empty[qr.slot], qr.turn ^ 1u, 0x441)) return;
                     if (elect_one()) {
                         mbar_arrive_expect_tx(&sh->q_full[qr.slot], (uint32_t)(a.nt * a.G * D * 2));
 #pragma unroll
                         for (int p = 0; p < D / 64; p++)
-                            tma_tile(x.q + qr.slot * C::TILE + p * C::PLANE, tq, p * 64, lh * a.G,
+                            tma_tile(x.q + qr.slot * C::TILE + p * C::PLANE, tq, p * 64, now.lh * a.G,
                                      now.t0 + now.node0 + i * a.nt, &sh->q_full[qr.slot]);
                     }
                     __syncwarp();
                     qr.next(2);
                 }
-                if (!ok) break;
-                at.k++;
-                at.pre += h.tiles + COST;
+                k++;
+                pre += h.tiles + COST;
             }
-            // the next item
-            have = seek(!begin);
+            // the next item of the range: part of an item that has tiles in it
+            for (bool raw = !first;; raw = false) {
+                it.node0 = k * 2 * a.nt;
+                it.lo = max(0, min(h.tiles, begin - pre - COST));
+                it.hi = max(0, min(h.tiles, end - pre - COST));
+                if (pre >= end) break;
+                if (it.node0 < h.nodes) {
+                    if (it.lo < it.hi) break;
+                    k++;
+                    pre += h.tiles + COST;
+                    continue;
+                }
+                k = 0;
+                if (++c >= a.C) break;
+                if (++lh == a.LH) {
+                    lh = 0;
+                    b++;
+                }
+                if (!raw) {
+                    r0 = __ldg(a.cu + b);
+                    r1 = __ldg(a.cu + b + 1);
+                    rn = __ldg(a.len + c);
+                }
+                h = Head(a, r0, r1, rn, a.status);
+            }
+            have = c < a.C && pre < end;
             if (have) {
+                it.c = c;
+                it.lh = lh;
+                it.t0 = h.t0;
+                it.nodes = h.nodes;
+                it.np = h.np;
+                it.len = h.len;
+                const int left = h.nodes - it.node0;
+                it.rows[0] = min(left, a.nt) * a.G;
+                it.rows[1] = left > a.nt ? min(left - a.nt, a.nt) * a.G : 0;
+                it.rec = -1;
+                if (it.lo > 0 || it.hi < h.tiles) {
+                    it.rec = 2 * (int)blockIdx.x + (it.lo == 0 ? 1 : 0);
+                    if (it.lo == 0 && lane == 0)  // the item's first part: it describes the item to the join
+                        a.join[blockIdx.x] = make_int4(c, it.node0, cta_of(sh->total, pre + COST + h.tiles - 1, n), 0);
+                }
                 ahead.start(a, it);
-                if (!begin && warp_test(&sh->w_empty[w.slot], w.turn ^ 1u)) post();
+                if (!first && warp_test(&sh->w_empty[w.slot], w.turn ^ 1u)) {
+                    posted = true;
+                    if (lane == 0) {
+                        sh->item[w.slot] = it;
+                        mbar_arrive(&sh->w_full[w.slot]);
+                    }
+                    w.next(ITEMS);
+                }
             }
-            if (begin) break;
+            if (first) break;
         }
     }
-    // the end: an item without rows
-    if (ok && warp_wait(&sh->w_empty[w.slot], w.turn ^ 1u, a.status, 0x444) && lane == 0) {
+    // the end: an item without rows, a tile that is none
+    if (!wait(&sh->w_empty[w.slot], w.turn ^ 1u, 0x444) || !wait(&sh->t_empty[tr.slot], tr.turn ^ 1u, 0x445)) return;
+    if (lane == 0) {
         sh->item[w.slot].rows[0] = 0;
         mbar_arrive(&sh->w_full[w.slot]);
+        sh->tile[tr.slot].live = END;
+        mbar_arrive(&sh->t_full[tr.slot]);
     }
 }
 
-// Warp 10: V, and the tiles whose V is to mend.
+// Warp 10: V.
 template <int D>
 __device__ void value_role(const Ctx<D> &x, const TreeArgs &a, const CUtensorMap *tv, const CUtensorMap *dv) {
-    using C = Cfg<D>;
     Shared *sh = x.sh;
-    const int lane = threadIdx.x & 31;
-    Ring vr, w, mr;
-    bool ok = true, early = false;
-    Groups groups, ahead;
-    for (;;) {
-        if (!early && !(ok = warp_wait(&sh->w_full[w.slot], w.turn, a.status, 0x446))) break;
-        const Item it = sh->item[w.slot];
-        if (it.rows[0] == 0) break;
-        if (early) groups = ahead;
-        else groups.start(a, it);
-        early = false;
-        Ring next = w;
-        next.next(ITEMS);
-        const int lh = it.c % a.LH;
 #pragma unroll 1
-        for (int j = it.lo; j < it.hi; j++) {
-            int32_t pg;
-            uint32_t wd;
-            bool draft;
-            groups.tile(j, j - it.lo, a.n_pages, a.status, pg, wd, draft);
-            const uint32_t live = __ballot_sync(0xFFFFFFFFu, wd != 0);
-            const uint32_t part = __ballot_sync(0xFFFFFFFFu, lane < 8 && (wd != 0xFFFFu || draft));
-            const uint32_t drafts = __ballot_sync(0xFFFFFFFFu, wd != 0 && draft);
-            if (!(ok = warp_wait(&sh->v_empty[vr.slot], vr.turn ^ 1u, a.status, 0x447))) break;
-            uint64_t *bar = part ? &sh->v_part[vr.slot] : &sh->v_full[vr.slot];
-            if (part) {
-                if (!(ok = warp_wait(&sh->m_empty[mr.slot], mr.turn ^ 1u, a.status, 0x443))) break;
-                Mend *md = &sh->mend[mr.slot];
-                if (lane < 8) md->word[lane] = (uint16_t)wd;
-                if (lane == 0) {
-                    md->slot = vr.slot;
-                    md->item = w.slot;
-                    md->draft = (int)drafts;
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh->m_full[mr.slot]);
-                mr.next(4);
-            }
-            if (lane < 8) sh->v_page[lane] = pg;
-            __syncwarp();
-            issue_tile<D>(x.v_slot(vr.slot), tv, dv, sh->v_page, live, drafts, lh, bar);
-            vr.next(C::VS);
-            if (!early && warp_test(&sh->w_full[next.slot], next.turn)) {
-                // the next item is there: its first pages
-                const Item after = sh->item[next.slot];
-                if (after.rows[0]) ahead.start(a, after);
-                early = true;
-            }
-        }
-        if (!ok) break;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->w_empty[w.slot]);
-        w = next;
-    }
-    // the end: a tile to mend without a slot
-    if (ok && warp_wait(&sh->m_empty[mr.slot], mr.turn ^ 1u, a.status, 0x445) && lane == 0) {
-        sh->mend[mr.slot].slot = -1;
-        mbar_arrive(&sh->m_full[mr.slot]);
+    for (Ring vr, tr;; vr.next(Cfg<D>::VS), tr.next(WORDS)) {
+        if (!warp_wait(&sh->t_full[tr.slot], tr.turn, a.status, 0x446)) return;
+        const Tile *t = &sh->tile[tr.slot];
+        const uint32_t live = t->live;
+        if (live == END) return;
+        if (!warp_wait(&sh->v_empty[vr.slot], vr.turn ^ 1u, a.status, 0x447)) return;
+        issue_tile<D>(x.v_slot(vr.slot), tv, dv, t->page, live, t->drafts, t->item_lh >> 8,
+                      t->part ? &sh->v_part[vr.slot] : &sh->v_full[vr.slot]);
+        if ((threadIdx.x & 31) == 0) mbar_arrive(&sh->t_empty[tr.slot]);
     }
 }
 
@@ -461,7 +426,7 @@ __device__ void mma_role(const Ctx<D> &x, bool neg) {
         for (int t = 0; t < n + ahead; t++) {
             const int j = t - ahead, vslot = (slot0 + j + 4) % C::VS, kslot = (slot0 + t) % C::KS;
             if (j >= 0) {
-                const int part = *(volatile uint32_t *)&sh->part[(tile_no + j) % WORDS] != 0;
+                const int part = *(volatile uint32_t *)&sh->tile[(tile_no + j) % WORDS].part != 0;
                 if (part) {
                     if (!x.wait(&sh->v_ready[vslot], r_turn >> vslot & 1u, 0x453)) return;
                     r_turn ^= 1u << vslot;
@@ -515,46 +480,44 @@ __device__ void mend_role(const Ctx<D> &x) {
     using C = Cfg<D>;
     Shared *sh = x.sh;
     const int lane = threadIdx.x & 31;
-    Ring mr;
+    // a row is D/8 pieces of 16 bytes: line row % 8 of each plane of block row / 8
+    constexpr int PIECES = D / 8, ROWS = 32 / PIECES;  // rows the warp takes at once
+    const int piece = (lane / 8 % (D / 64)) * 64 + lane % 8;
     uint32_t turn = 0;  // v_part: a bit for each slot
-    for (;; mr.next(4)) {
-        if (!x.wait(&sh->m_full[mr.slot], mr.turn, 0x460)) return;
-        const Mend md = sh->mend[mr.slot];
-        if (md.slot < 0) return;
-        if (!x.wait(&sh->v_part[md.slot], turn >> md.slot & 1u, 0x461)) return;
-        turn ^= 1u << md.slot;
-        // a row is D/8 pieces of 16 bytes: line row % 8 of each plane of block row / 8
-        constexpr int PIECES = D / 8, ROWS = 32 / PIECES;  // rows the warp takes at once
-        const int piece = (lane / 8 % (D / 64)) * 64 + lane % 8;
-        auto at = [&](int r) {  // this lane's piece of the r-th ROWS rows of a group
-            const int row = r * ROWS + lane / PIECES;
-            return (row >> 3) * (C::BLOCK / 16) + (row & 7) * 8;
-        };
-        bool odd = false;
 #pragma unroll 1
-        for (int g = 0; g < 8; g++) {
-            const uint32_t word = md.word[g];
-            uint4 *group = reinterpret_cast<uint4 *>(x.v_slot(md.slot) + g * C::GROUP) + piece;
-            const bool draft = md.draft >> g & 1;
-            if (word == 0xFFFFu && !draft) continue;
+    for (Ring vr, tr;; vr.next(C::VS), tr.next(WORDS)) {
+        if (!x.wait(&sh->t_full[tr.slot], tr.turn, 0x460)) return;
+        const Tile *t = &sh->tile[tr.slot];
+        const uint32_t live = t->live, drafts = t->drafts;
+        if (live == END) return;
+        if (t->part) {
+            if (!x.wait(&sh->v_part[vr.slot], turn >> vr.slot & 1u, 0x461)) return;
+            turn ^= 1u << vr.slot;
+            bool odd = false;
+#pragma unroll 1
+            for (int g = 0; g < 8; g++) {
+                const uint32_t word = t->word[g];
+                const bool draft = drafts >> g & 1;
+                if (word == 0xFFFFu && !draft) continue;
+                uint4 *group = reinterpret_cast<uint4 *>(x.v_slot(vr.slot) + g * C::GROUP) + piece;
 #pragma unroll 2
-            for (int r = 0; r < 16 / ROWS; r++) {
-                uint4 *p = group + at(r), v = make_uint4(0, 0, 0, 0);
-                const bool in = word >> (r * ROWS + lane / PIECES) & 1u;
-                if (draft && in) {
-                    v = *p;
-                    odd |= drop_odd(v);
+                for (int r = lane / PIECES; r < 16; r += ROWS) {
+                    uint4 *p = group + (r >> 3) * (C::BLOCK / 16) + (r & 7) * 8, v = make_uint4(0, 0, 0, 0);
+                    const bool in = word >> r & 1u;
+                    if (draft && in) {
+                        v = *p;
+                        odd |= drop_odd(v);
+                    }
+                    if (draft || !in) *p = v;
                 }
-                if (draft || !in) *p = v;
             }
+            if (odd) atomicOr(&sh->item[t->item_lh & 255u].odd, 1);
+            fence_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh->v_ready[vr.slot]);
         }
-        if (odd) atomicOr(&sh->item[md.item].odd, 1);
-        fence_async_shared();
+        if (lane == 0) mbar_arrive(&sh->t_empty[tr.slot]);
         __syncwarp();
-        if (lane == 0) {
-            mbar_arrive(&sh->v_ready[md.slot]);
-            mbar_arrive(&sh->m_empty[mr.slot]);
-        }
     }
 }
 
@@ -566,6 +529,7 @@ __device__ void softmax_role(const Ctx<D> &x, const TreeArgs &a) {
     const uint32_t lanes = (uint32_t)(row & 96) << 16;
     const uint32_t ts = sh->tmem + TM_S + i * 128 + lanes, o0 = sh->tmem + TM_O + lanes, to = o0 + i * D;
     const float qscale = fabsf(a.qscale);
+    const int row_node = row / a.G, row_g = row % a.G;
     uint32_t s_turn = 0, d_turn[2] = {0, 0}, x_turn = 0;  // d_turn: parity of the next product to complete
     int tile_no = 0;
     uint32_t flip = 0;
@@ -577,7 +541,7 @@ __device__ void softmax_role(const Ctx<D> &x, const TreeArgs &a) {
         const bool two = it.rows[1] > 0;
         const int n = it.hi - it.lo, rows = two ? it.rows[i] : it.rows[0];
         const bool warp_here = (row & 96) < rows;  // some row of this warp counts
-        const int node = it.node0 + (two ? i * a.nt : 0) + row / a.G;
+        const int node = it.node0 + (two ? i * a.nt : 0) + row_node;
         unsigned long long mask = 0;
         if (row < rows) mask = __ldg(a.mask + it.t0 + node);
         float m = -INFINITY, l = 0.f;
@@ -589,7 +553,7 @@ __device__ void softmax_role(const Ctx<D> &x, const TreeArgs &a) {
             if (warp_here) {
                 tc_fence_after();
                 const Tile *t = &sh->tile[(tile_no + j) % WORDS];
-                const uint32_t part = *(volatile const uint32_t *)&sh->part[(tile_no + j) % WORDS];
+                const uint32_t part = *(volatile const uint32_t *)&t->part;
                 auto done = [&] { return x.wait(&sh->o_done[i], d_turn[i] ^ 1u, 0x472); };
                 uint32_t bits[4];
                 if (part) {
@@ -600,14 +564,16 @@ __device__ void softmax_role(const Ctx<D> &x, const TreeArgs &a) {
                     bits[3] = w4.w;
                     const int first = it.np - (it.lo + j) * 8;  // group of the tile with which the draft begins
                     if (first < 8) {
-#pragma unroll
-                        for (int g = 0; g < 8; g++) {
-                            const int d = g - first;
-                            if (d >= 0) {
-                                const uint32_t see = d < 4 ? (uint32_t)(mask >> (16 * d)) & 0xFFFFu : 0u;
-                                bits[g >> 1] &= g & 1 ? see << 16 | 0xFFFFu : see | 0xFFFF0000u;
-                            }
-                        }
+                        // the draft's 64 bits from bit 16 * first of the tile's 128 on
+                        const int at = 16 * first;
+                        const unsigned long long lo = at < 64 ? (at < 0 ? mask >> -at : mask << at) : 0ull;
+                        const unsigned long long hi = at >= 64 ? mask << (at - 64) : at > 0 ? mask >> (64 - at) : 0ull;
+                        const unsigned long long c_lo = at >= 64 ? ~0ull : at > 0 ? (1ull << at) - 1ull : 0ull;
+                        const unsigned long long c_hi = at > 64 ? (1ull << (at - 64)) - 1ull : 0ull;
+                        bits[0] &= (uint32_t)(lo | c_lo);
+                        bits[1] &= (uint32_t)((lo | c_lo) >> 32);
+                        bits[2] &= (uint32_t)(hi | c_hi);
+                        bits[3] &= (uint32_t)((hi | c_hi) >> 32);
                     }
                 }
                 auto columns = [&](int c) { return c < 2 ? (c ? bits[1] : bits[0]) : (c == 2 ? bits[2] : bits[3]); };
@@ -651,15 +617,14 @@ __device__ void softmax_role(const Ctx<D> &x, const TreeArgs &a) {
             const int odd = *(volatile int *)&sh->item[w.slot].odd;
             const bool here = row < rows;
             const bool none = m == -INFINITY;
-            const int lh = it.c % a.LH;
-            const int64_t at = (int64_t)(it.t0 + node) * a.LH * a.G + (int64_t)lh * a.G + row % a.G;  // row of q and out
+            const int64_t at = (int64_t)(it.t0 + node) * a.LH * a.G + it.lh * a.G + row_g;  // row of q and out
             const float inv = it.rec >= 0 ? 1.f : none ? 0.f : __fdividef(1.f, l);
             float *rec = nullptr;
             if (it.rec >= 0) rec = a.rec + ((int64_t)it.rec * a.rec_tiles + (two ? i : 0)) * (QR * (D + 2)) + row;
             if (__any_sync(0xFFFFFFFFu, odd)) {
                 scale0 = fmaxf(scale0, 0x1p-100f);  // infinite values pass, finite ones vanish as with 0
                 for (int d = 0; d < it.nodes; d++)
-                    add_odd<D>(two ? to : o0, static_cast<const __nv_bfloat16 *>(a.v_draft) + ((int64_t)(it.t0 + d) * a.LH + lh) * D,
+                    add_odd<D>(two ? to : o0, static_cast<const __nv_bfloat16 *>(a.v_draft) + ((int64_t)(it.t0 + d) * a.LH + it.lh) * D,
                                here && (mask >> d & 1ull), c_lo, c_hi);
             }
             const uint32_t rows_here = __ballot_sync(0xFFFFFFFFu, here);
@@ -719,7 +684,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < ITEMS; s++) {
             mbar_init(&sh.w_full[s], 1);
-            mbar_init(&sh.w_empty[s], 10);  // products, V, eight softmax warps
+            mbar_init(&sh.w_empty[s], 9);  // products, eight softmax warps
         }
         for (int s = 0; s < 4; s++) {
             mbar_init(&sh.k_full[s], 1);
@@ -728,8 +693,10 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             mbar_init(&sh.v_empty[s], 1);
             mbar_init(&sh.v_part[s], 1);
             mbar_init(&sh.v_ready[s], 1);
-            mbar_init(&sh.m_full[s], 1);
-            mbar_init(&sh.m_empty[s], 1);
+        }
+        for (int s = 0; s < WORDS; s++) {
+            mbar_init(&sh.t_full[s], 1);
+            mbar_init(&sh.t_empty[s], 2);  // V, mending
         }
         for (int i = 0; i < 2; i++) {
             mbar_init(&sh.q_full[i], 1);
