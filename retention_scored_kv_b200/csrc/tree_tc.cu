@@ -36,10 +36,25 @@ constexpr int ITEMS = 4;      // ring of items
 // tile are evenly spaced, as one descriptor needs them.
 template <int D>
 struct Cfg {
-    static constexpr int TILE = TcCfg<D>::TILE, PLANE = TcCfg<D>::PLANE;
+    static constexpr int TILE = TcCfg<D>::TILE;
     static constexpr int GROUP = PAGE * D * 2, BLOCK = GROUP / 2;
-    static constexpr int KS = D == 128 ? 2 : 4, VS = KS;  // K and V tiles in flight
-    static constexpr int SMEM = (2 + KS + VS) * TILE + 1024; // two query tiles; alignment of the swizzle's period
+    static constexpr int ROOM = 227 * 1024 - 1024;  // of shared memory, less the alignment of the swizzle's period
+};
+
+// Shared memory: two query tiles of as many rows as the call's tiles have (the
+// products read 128 rows from there on: what lies behind only gives rows that do
+// not count), and slots for K and V tiles with the rest.  More slots are more
+// bytes in flight: 2 + 2 with 128 rows of D = 128, 2 + 3 with 96, 3 + 3 up to 40.
+struct Room {
+    int plane, tile;  // bytes of 64 columns of a query tile, and of the tile
+    int ks, vs;       // slots, at most 4 each
+    __host__ __device__ Room(int rows, int D, int room) {
+        plane = (rows + 7) / 8 * 1024;
+        tile = plane * (D / 64);
+        const int n = (room - 2 * tile) / (128 * D * 2);
+        ks = n / 2 > 4 ? 4 : n / 2;
+        vs = n - ks > 4 ? 4 : n - ks;
+    }
 };
 
 __host__ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
@@ -83,9 +98,12 @@ struct Ctx {
     Shared *sh;
     unsigned char *q, *kv;
     int32_t *status;
-    __device__ bool wait(uint64_t *bar, uint32_t parity, int site) const { return tc_wait(bar, parity, status, site); }
-    __device__ unsigned char *k_slot(int i) const { return kv + (size_t)i * Cfg<D>::TILE; }
-    __device__ unsigned char *v_slot(int i) const { return kv + (size_t)(Cfg<D>::KS + i) * Cfg<D>::TILE; }
+    Room room;
+    __device__ bool wait(uint64_t *bar, uint32_t parity, int site) const { return wait_on(bar, parity, status, site); }
+    // in line, for the waits that every tile's path goes through
+    __device__ bool wait_near(uint64_t *bar, uint32_t parity, int site) const { return tc_wait(bar, parity, status, site); }
+    __device__ unsigned char *k_slot(int i) const { return kv + i * Cfg<D>::TILE; }
+    __device__ unsigned char *v_slot(int i) const { return kv + (room.ks + i) * Cfg<D>::TILE; }
 };
 
 // Key tiles of head c and items it is cut into.
@@ -276,7 +294,7 @@ __device__ void load_role(const Ctx<D> &x, const TreeArgs &a, int n, const CUten
                 tr.next(WORDS);
                 if (!wait(&sh->k_empty[kr.slot], kr.turn ^ 1u, 0x442)) return;
                 issue_tile<D>(x.k_slot(kr.slot), tk, dk, t->page, live, drafts, now.lh, &sh->k_full[kr.slot]);
-                kr.next(C::KS);
+                kr.next(x.room.ks);
                 if (j > now.lo) continue;
                 // the item's one or two query tiles, behind its first key tile: their
                 // slots are free only when the products of the item before are done
@@ -287,7 +305,7 @@ __device__ void load_role(const Ctx<D> &x, const TreeArgs &a, int n, const CUten
                         mbar_arrive_expect_tx(&sh->q_full[qr.slot], (uint32_t)(a.nt * a.G * D * 2));
 #pragma unroll
                         for (int p = 0; p < D / 64; p++)
-                            tma_tile(x.q + qr.slot * C::TILE + p * C::PLANE, tq, p * 64, now.lh * a.G,
+                            tma_tile(x.q + qr.slot * x.room.tile + p * x.room.plane, tq, p * 64, now.lh * a.G,
                                      now.t0 + now.node0 + i * a.nt, &sh->q_full[qr.slot]);
                     }
                     __syncwarp();
@@ -366,7 +384,7 @@ template <int D>
 __device__ void value_role(const Ctx<D> &x, const TreeArgs &a, const CUtensorMap *tv, const CUtensorMap *dv) {
     Shared *sh = x.sh;
 #pragma unroll 1
-    for (Ring vr, tr;; vr.next(Cfg<D>::VS), tr.next(WORDS)) {
+    for (Ring vr, tr;; vr.next(x.room.vs), tr.next(WORDS)) {
         if (!warp_wait(&sh->t_full[tr.slot], tr.turn, a.status, 0x446)) return;
         const Tile *t = &sh->tile[tr.slot];
         const uint32_t live = t->live;
@@ -380,10 +398,10 @@ __device__ void value_role(const Ctx<D> &x, const TreeArgs &a, const CUtensorMap
 
 // ---------------------------------------------------------- warp 9: products ----
 template <int D>
-__device__ __forceinline__ void mma_scores(uint32_t s, uint64_t q, uint64_t k, uint32_t idesc) {
+__device__ __forceinline__ void mma_scores(uint32_t s, uint64_t q, int q_plane, uint64_t k, uint32_t idesc) {
 #pragma unroll
     for (int e = 0; e < D / 16; e++)
-        mma_ss(s, desc_at(q, (e / 4) * Cfg<D>::PLANE + (e % 4) * 32), desc_at(k, (e / 4) * 1024 + (e % 4) * 32), idesc, e > 0);
+        mma_ss(s, desc_at(q, (e / 4) * q_plane + (e % 4) * 32), desc_at(k, (e / 4) * 1024 + (e % 4) * 32), idesc, e > 0);
 }
 
 template <int D>
@@ -401,7 +419,7 @@ __device__ void mma_role(const Ctx<D> &x, bool neg) {
     const uint32_t tmem = sh->tmem;
     const uint32_t qk = mma_desc(QR, KR, false, neg), pv = mma_desc(QR, D, true, false);
     Ring w, qr;
-    int slot0 = 0, tile_no = 0;  // key tiles so far: mod KS (and VS), mod WORDS
+    int kslot = 0, vslot = 0, tile_no = 0;  // slots of the next K and V; key tiles so far, mod WORDS
     uint32_t k_turn = 0, v_turn = 0, r_turn = 0, q_turn = 0;  // k_full, v_full, v_ready, q_full: a bit for each slot
     uint32_t p_turn = 0, f_turn = 0;                          // p_full: a bit for each tile; o_free
     const uint64_t q_desc = tile_desc(smem_u32(x.q), 16), k_desc = tile_desc(smem_u32(x.k_slot(0)), 16, C::BLOCK),
@@ -424,7 +442,7 @@ __device__ void mma_role(const Ctx<D> &x, bool neg) {
         const int ahead = two ? 1 : 2;
 #pragma unroll 1
         for (int t = 0; t < n + ahead; t++) {
-            const int j = t - ahead, vslot = (slot0 + j + 4) % C::VS, kslot = (slot0 + t) % C::KS;
+            const int j = t - ahead;
             if (j >= 0) {
                 const int part = *(volatile uint32_t *)&sh->tile[(tile_no + j) % WORDS].part != 0;
                 if (part) {
@@ -445,10 +463,10 @@ __device__ void mma_role(const Ctx<D> &x, bool neg) {
                 const uint32_t o = tmem + TM_O + i * D, p = tmem + TM_S + i * 128;
                 if (j >= 0) {
                     const uint64_t v = desc_at(v_desc, vslot * C::TILE);
-                    if (!x.wait(&sh->p_full[i][0], p_turn >> i & 1u, 0x456)) return;
+                    if (!x.wait_near(&sh->p_full[i][0], p_turn >> i & 1u, 0x456)) return;
                     tc_fence_after();
                     mma_output<D>(o, p, v, pv, 0, j < ahead);
-                    if (!x.wait(&sh->p_full[i][1], p_turn >> i & 1u, 0x457)) return;
+                    if (!x.wait_near(&sh->p_full[i][1], p_turn >> i & 1u, 0x457)) return;
                     p_turn ^= 1u << i;
                     tc_fence_after();
                     mma_output<D>(o, p, v, pv, 1, false);
@@ -461,15 +479,18 @@ __device__ void mma_role(const Ctx<D> &x, bool neg) {
                     }
                     const int qs = q ? qs1 : qs0;
                     tc_fence_after();
-                    mma_scores<D>(p, desc_at(q_desc, qs * C::TILE), desc_at(k_desc, kslot * C::TILE), qk);
+                    mma_scores<D>(p, desc_at(q_desc, qs * x.room.tile), x.room.plane, desc_at(k_desc, kslot * C::TILE), qk);
                     mma_commit(&sh->s_full[i]);
                     if (q == two) mma_commit(&sh->k_empty[kslot]);
                     if (t == n - 1) mma_commit(&sh->q_empty[qs]);
                 }
             }
-            if (j >= 0) mma_commit(&sh->v_empty[vslot]);
+            if (j >= 0) {
+                mma_commit(&sh->v_empty[vslot]);
+                vslot = vslot + 1 == x.room.vs ? 0 : vslot + 1;
+            }
+            if (t < n) kslot = kslot + 1 == x.room.ks ? 0 : kslot + 1;
         }
-        slot0 = (slot0 + n) % C::KS;
         tile_no = (tile_no + n) % WORDS;
     }
 }
@@ -483,9 +504,10 @@ __device__ void mend_role(const Ctx<D> &x) {
     // a row is D/8 pieces of 16 bytes: line row % 8 of each plane of block row / 8
     constexpr int PIECES = D / 8, ROWS = 32 / PIECES;  // rows the warp takes at once
     const int piece = (lane / 8 % (D / 64)) * 64 + lane % 8;
+    const uint32_t mine = (ROWS == 2 ? 0x5555u : 0x1111u) << (lane / PIECES);
     uint32_t turn = 0;  // v_part: a bit for each slot
 #pragma unroll 1
-    for (Ring vr, tr;; vr.next(C::VS), tr.next(WORDS)) {
+    for (Ring vr, tr;; vr.next(x.room.vs), tr.next(WORDS)) {
         if (!x.wait(&sh->t_full[tr.slot], tr.turn, 0x460)) return;
         const Tile *t = &sh->tile[tr.slot];
         const uint32_t live = t->live, drafts = t->drafts;
@@ -500,15 +522,18 @@ __device__ void mend_role(const Ctx<D> &x) {
                 const bool draft = drafts >> g & 1;
                 if (word == 0xFFFFu && !draft) continue;
                 uint4 *group = reinterpret_cast<uint4 *>(x.v_slot(vr.slot) + g * C::GROUP) + piece;
-#pragma unroll 2
-                for (int r = lane / PIECES; r < 16; r += ROWS) {
-                    uint4 *p = group + (r >> 3) * (C::BLOCK / 16) + (r & 7) * 8, v = make_uint4(0, 0, 0, 0);
-                    const bool in = word >> r & 1u;
-                    if (draft && in) {
-                        v = *p;
-                        odd |= drop_odd(v);
+                auto row = [&](int r) { return group + (r >> 3) * (C::BLOCK / 16) + (r & 7) * 8; };
+                // every ROWS-th row is this part of the warp's: those that do not count
+#pragma unroll 1
+                for (uint32_t gone = ~word & mine; gone; gone &= gone - 1) *row(__ffs(gone) - 1) = make_uint4(0, 0, 0, 0);
+                if (!draft) continue;
+#pragma unroll 1
+                for (uint32_t left = word & mine; left; left &= left - 1) {
+                    uint4 *p = row(__ffs(left) - 1), v = *p;
+                    if (drop_odd(v)) {
+                        odd = true;
+                        *p = v;
                     }
-                    if (draft || !in) *p = v;
                 }
             }
             if (odd) atomicOr(&sh->item[t->item_lh & 255u].odd, 1);
@@ -548,7 +573,7 @@ __device__ void softmax_role(const Ctx<D> &x, const TreeArgs &a) {
         int mine = 0;
 #pragma unroll 1
         for (int j = two ? 0 : i; j < n; j += two ? 1 : 2, mine++) {
-            if (!x.wait(&sh->s_full[i], s_turn, 0x471)) return;
+            if (!x.wait_near(&sh->s_full[i], s_turn, 0x471)) return;
             s_turn ^= 1u;
             if (warp_here) {
                 tc_fence_after();
@@ -748,7 +773,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const Ctx<D> x{&sh, tiles, tiles + 2 * Cfg<D>::TILE, a.status};
+    const Room room(a.nt * a.G, D, Cfg<D>::ROOM - (int)sizeof(Shared) - 256);
+    const Ctx<D> x{&sh, tiles, tiles + 2 * room.tile, a.status, room};
     if (good && sh.begin < sh.end) {
         if (warp < 8) softmax_role<D>(x, a);
         else if (warp == 8) load_role<D>(x, a, n, &tq, &tk, &dk);
@@ -809,9 +835,13 @@ __global__ void __launch_bounds__(QR) tree_join_kernel(const TreeArgs a) {
 template <int D>
 cudaError_t launch(const TreeArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                    const CUtensorMap &dk, const CUtensorMap &dv, cudaStream_t s) {
-    cudaError_t e = cudaFuncSetAttribute(tree_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM);
+    const Room room(a.nt * a.G, D, Cfg<D>::ROOM - (int)sizeof(Shared) - 256);
+    // as much whatever the rows: a products' read of 128 rows stays inside
+    const int smem = Cfg<D>::ROOM - (int)sizeof(Shared) - 256 + 1024;
+    if (room.ks < 2 || room.vs < 2) return cudaErrorNotSupported;
+    cudaError_t e = cudaFuncSetAttribute(tree_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    tree_tc_kernel<D><<<TREE_CTAS, TC_THREADS, Cfg<D>::SMEM, s>>>(a, tq, tk, tv, dk, dv);
+    tree_tc_kernel<D><<<TREE_CTAS, TC_THREADS, smem, s>>>(a, tq, tk, tv, dk, dv);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     return launch_after(tree_join_kernel<D>, dim3(TREE_CTAS, a.rec_tiles, D / 32), QR, 0, s, a);
 }
