@@ -143,3 +143,26 @@ def test_captured_on_another_stream_and_replayed_on_new_values(rkv, dtype):
         graph.replay()
         check(q, k, v, out, lse, ls, 0.1)
     assert ws.status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [0.0, -0.4])
+def test_scales_of_zero_and_below(rkv, scale, dtype):
+    cache, ws = shape_cache(rkv, 2, 2, 4, 128, dtype)
+    q, k, v = inputs(340, 2, 4, 128, dtype)
+    out, lse = torch.empty(340, 4, 128, dtype=q.dtype, device="cuda"), torch.empty(340, 4, device="cuda")
+    rkv.prompt_attn(cache, starts([300, 40]), q, k, v, scale, out, lse, ws)
+    check(q, k, v, out, lse, [300, 40], scale)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_many_sequences_and_more_work_than_one_round(rkv, dtype):
+    """1024 sequences, most of them empty or short, and several pieces of work for each SM."""
+    lens = [(i * 37) % 11 if i % 5 else 0 for i in range(1021)] + [700, 1, 513]
+    cache, ws = shape_cache(rkv, 1024, 1, 2, 64, dtype)
+    T = sum(lens)
+    q, k, v = inputs(T, 1, 2, 64, dtype)
+    out, lse = torch.empty(T, 2, 64, dtype=q.dtype, device="cuda"), torch.empty(T, 2, device="cuda")
+    rkv.prompt_attn(cache, starts(lens), q, k, v, 0.125, out, lse, ws)
+    check(q, k, v, out, lse, lens, 0.125)
+    assert ws.status() == 0

@@ -228,6 +228,19 @@ def test_captured_and_replayed_with_other_trees(rkv, dtype):
     assert ws.status() == 0
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [0.0, -0.4])
+def test_scales_of_zero_and_below(rkv, scale, dtype):
+    """0: the mean of what is attended; negative: the order of the logits turns round."""
+    nodes = [5, 40]
+    dc, cache, ws = make(rkv, [200, 40, 0, 129], 2, 1, 2, 4, 64, dtype, 40)
+    q, kd, vd = draft(45, 1, 2, 4, 64, dtype)
+    mask = tree_masks(nodes, blank=(1,))
+    out, lse = outputs(q)
+    rkv.tree_attn(cache, starts(nodes), q, kd, vd, mask, scale, None, out, lse, ws, max_nodes=40)
+    check(dc, q, kd, vd, mask, nodes, scale, out, lse)
+
+
 def test_calls_of_different_sizes_share_a_workspace(rkv):
     """Small trees after large ones and back, in turn with the decode step's calls."""
     for dtype in ("bf16", "f32"):
