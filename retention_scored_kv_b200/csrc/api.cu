@@ -124,6 +124,7 @@ void layout_for(const rkv_cache_t &c, int sel_groups_x_waves, WsLayout *L) {
     L->seq_plan = take(8, 256);
     L->seq_base = take((size_t)C * 4, 256);
     L->seq_pop = take((size_t)C * 4, 256);
+    L->seq_old = take((size_t)C * 4, 256);
     L->total = take(0, 256);
 }
 
@@ -1051,6 +1052,7 @@ RKV_API int rkv_fork_sequences(const rkv_cache_t *cache, const int32_t *parent, 
     a.plan = at<int32_t>(ws, L.seq_plan);
     a.base = at<int32_t>(ws, L.seq_base);
     a.pop = at<int32_t>(ws, L.seq_pop);
+    a.old = at<int32_t>(ws, L.seq_old);
     a.B = cache->B;
     a.LH = cache->L * cache->H;
     a.C = cache->B * a.LH;

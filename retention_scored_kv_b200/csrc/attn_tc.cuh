@@ -158,9 +158,11 @@ __device__ __forceinline__ bool softmax_tile(uint32_t ts, uint32_t to, bool firs
     }
     if (masked) tmem_wait_st();
     tmem_ld32(a, ts);
-    if (__any_sync(0xFFFFFFFFu, first || !((mt - m) * qscale <= RESCALE || mt == -INFINITY))) {
-        // the whole warp moves to its new maxima (O is read and written by warps)
-        float mn = max_nan(m, mt, mt);
+    const bool grow = first || !((mt - m) * qscale <= RESCALE || mt == -INFINITY);
+    if (__any_sync(0xFFFFFFFFu, grow)) {
+        // O is read and written by warps; a row that need not stays as it is, so
+        // that its result does not depend on the rows beside it
+        float mn = grow ? max_nan(m, mt, mt) : m;
         if (mn == INFINITY) mn = NAN;
         if (!first) {
             const float f = mn == -INFINITY ? 1.f : ex2((m - mn) * qscale);

@@ -50,6 +50,7 @@ struct WsLayout {
     size_t seq_plan;      // int32 [2] outcome of a sequence plan: go, free pages after it
     size_t seq_base;      // int32 [C] lengths a sequence operator works from
     size_t seq_pop;       // int32 [C] stack index of the first page each head takes
+    size_t seq_old;       // int32 [C] lengths before a fork
     size_t total;
 };
 
@@ -388,8 +389,9 @@ struct ForkArgs {
     float *lb_pool;
     int32_t *block_table, *len, *free_stack, *free_top;
     const int32_t *parent;     // [B]
-    int32_t *status, *plan, *base, *pop;
+    int32_t *status, *plan, *base, *pop, *old;
     int B, LH, C, max_pages, n_pages;
+    int chunks;                // CTAs of each (layer, head)
 };
 cudaError_t launch_fork(const ForkArgs &a, int row_bytes, cudaStream_t s);
 

@@ -166,3 +166,24 @@ def test_many_sequences_and_more_work_than_one_round(rkv, dtype):
     rkv.prompt_attn(cache, starts(lens), q, k, v, 0.125, out, lse, ws)
     check(q, k, v, out, lse, lens, 0.125)
     assert ws.status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_nothing_to_attend_and_nan_keys(rkv, dtype):
+    """Only empty sequences: nothing is written.  A NaN key makes the rows that attend it NaN, and no others."""
+    cache, ws = shape_cache(rkv, 2, 1, 2, 128, dtype)
+    q, k, v = inputs(350, 1, 2, 128, dtype, seed=3)
+    out, lse = torch.full((350, 2, 128), 7.0, dtype=q.dtype, device="cuda"), torch.full((350, 2), 7.0, device="cuda")
+    rkv.prompt_attn(cache, starts([0, 0], first=5), q, k, v, 0.1, out, lse, ws)
+    assert bool((out == 7).all()) and bool((lse == 7).all()) and ws.status() == 0
+    k = k.clone()
+    k[140, 0, 77] = math.nan
+    rkv.prompt_attn(cache, starts([300, 50]), q, k, v, 0.1, out, lse, ws)
+    hit = torch.zeros(350, dtype=torch.bool, device="cuda")
+    hit[140:300] = True
+    assert bool(torch.isnan(out[hit].float()).all()) and bool(torch.isnan(lse[hit]).all())
+    k[140, 0, 77] = 0
+    keep_out, keep_lse = out.clone(), lse.clone()
+    rkv.prompt_attn(cache, starts([300, 50]), q, k, v, 0.1, out, lse, ws)
+    check(q, k, v, out, lse, [300, 50], 0.1)
+    assert torch.equal(out[~hit], keep_out[~hit]) and torch.equal(lse[~hit], keep_lse[~hit])

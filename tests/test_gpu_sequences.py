@@ -163,6 +163,17 @@ def test_fork_of_64_sequences_and_one(rkv):
         want.assert_same(dc)
 
 
+def test_fork_in_a_long_and_nearly_empty_table(rkv):
+    have = [0, 900, 16, 1, 9, 33, 2000, 5]
+    dc, cache, ws = make(rkv, have, 2, max_pages=5000, spare=300)
+    want = ListCache(dc)
+    for parent in ([0, 0], [1, 0], [-1, 1], [1, 1]):
+        want.fork(4, parent)
+        rkv.fork_sequences(cache, torch.tensor(parent, dtype=torch.int32, device="cuda"), ws)
+        want.assert_same(dc)
+    assert ws.status() == 0
+
+
 def test_fork_without_room_or_with_bad_parents_changes_nothing(rkv):
     have = [40, 0, 16, 1, 9, 9, 9, 9]
     dc, cache, ws = make(rkv, have, 2, spare=0)

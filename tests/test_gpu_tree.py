@@ -254,3 +254,12 @@ def test_calls_of_different_sizes_share_a_workspace(rkv):
             o2 = torch.empty(1, 2, 8, 128, device="cuda")
             rkv.paged_decode_attn(cache, q[:1].float().contiguous(), 0.09, None, o2, None, None, ws)
         assert ws.status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_no_trees_at_all(rkv, dtype):
+    dc, cache, ws = make(rkv, [200, 40, 0, 129], 2, 1, 2, 4, 64, dtype, 8)
+    q, kd, vd = draft(3, 1, 2, 4, 64, dtype)
+    out, lse = outputs(q)
+    rkv.tree_attn(cache, starts([0, 0], first=1), q, kd, vd, tree_masks([3]), 0.1, None, out, lse, ws, max_nodes=8)
+    assert bool((out == 7).all()) and bool((lse == 7).all()) and ws.status() == 0
