@@ -182,10 +182,10 @@ class Cache:
                    B, L, H, Hq)
 
     def struct(self) -> CacheStruct:
-        return CacheStruct(_ptr(self.k_pool), _ptr(self.v_pool), _ptr(self.pos_pool), _ptr(self.lb_pool),
-                           _ptr(self.block_table), _ptr(self.len), _ptr(self.free_stack), _ptr(self.free_top),
-                           self.B, self.L, self.H, self.Hq, self.D, PAGE, self.n_pages, self.max_pages,
-                           self.dtype_code)
+        k, table = self.k_pool, self.block_table
+        return CacheStruct(_ptr(k), _ptr(self.v_pool), _ptr(self.pos_pool), _ptr(self.lb_pool), _ptr(table),
+                           _ptr(self.len), _ptr(self.free_stack), _ptr(self.free_top), self.B, self.L, self.H, self.Hq,
+                           k.shape[-1], PAGE, k.shape[0], table.shape[1], self.dtype_code)
 
 
 @dataclass
@@ -405,11 +405,12 @@ def _packed(name: str, x: torch.Tensor, shape: tuple, dtype: torch.dtype, device
 def _on(device: torch.device, stream: torch.cuda.Stream | None, fn, *args):
     """fn(*args, stream) on the tensors' own device, which need not be the current one; ``stream`` or that
     device's current stream."""
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    if device.index == torch.cuda.current_device():
-        return _check(fn(*args, s.cuda_stream))
+    idx = device.index
+    raw = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(idx)
+    if idx == torch._C._cuda_getDevice():
+        return _check(fn(*args, raw))
     with torch.cuda.device(device):
-        _check(fn(*args, s.cuda_stream))
+        _check(fn(*args, raw))
 
 
 def prompt_attn(cache: Cache, cu: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: float,

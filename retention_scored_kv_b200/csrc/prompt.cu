@@ -10,13 +10,13 @@
 namespace rkv {
 namespace {
 
-// One CTA per (16*R query rows, query head): FFMA products, see serve.cuh.
-template <int D, int R>
-__global__ void __launch_bounds__(FT_THREADS) prompt_ffma_kernel(const PromptArgs a) {
+// One CTA per (T/16*R query rows, query head): FFMA products, see serve.cuh.
+template <int D, int R, int T>
+__global__ void __launch_bounds__(T) prompt_ffma_kernel(const PromptArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];
-    FTile<D, R> &t = *reinterpret_cast<FTile<D, R> *>(smem);
-    int32_t *s_cu = reinterpret_cast<int32_t *>(smem + sizeof(FTile<D, R>));
-    constexpr int ROWS = 16 * R;
+    FTile<D, T / 16 * R> &t = *reinterpret_cast<FTile<D, T / 16 * R> *>(smem);
+    int32_t *s_cu = reinterpret_cast<int32_t *>(smem + sizeof(FTile<D, T / 16 * R>));
+    constexpr int ROWS = T / 16 * R;
     __shared__ SeqTile s_tile;
     if (!load_offsets(a.cu, a.B, a.n_tokens, a.n_tokens, s_cu, a.status)) return;
     const int tile = blockIdx.x / a.Hq, hq = blockIdx.x % a.Hq;
@@ -34,7 +34,7 @@ __global__ void __launch_bounds__(FT_THREADS) prompt_ffma_kernel(const PromptArg
     const float *k = static_cast<const float *>(a.k) + (int64_t)h * D;
     const float *v = static_cast<const float *>(a.v) + (int64_t)h * D;
     constexpr int V4 = D / 4;
-    for (int i = threadIdx.x; i < ROWS * V4; i += FT_THREADS) {
+    for (int i = threadIdx.x; i < ROWS * V4; i += T) {
         const int r = i / V4, d = i % V4 * 4;
         const float4 x = r0 + r < n ? ld4(q + (t0 + r0 + r) * a.q_stride + d) : make_float4(0.f, 0.f, 0.f, 0.f);
         *reinterpret_cast<float4 *>(&t.q[r][d]) = x;
@@ -43,12 +43,12 @@ __global__ void __launch_bounds__(FT_THREADS) prompt_ffma_kernel(const PromptArg
     st.init();
     const int last = min(r0 + ROWS, n);
     // a key tile's K and V are on their way to registers while the tile before is worked on
-    constexpr int N = FT_KEYS * V4 / FT_THREADS;
+    constexpr int N = FT_KEYS * V4 / T;
     float4 kr[N], vr[N];
     auto load = [&](int j0) {
 #pragma unroll
         for (int i = 0; i < N; i++) {
-            const int e = i * FT_THREADS + threadIdx.x, r = e / V4, d = e % V4 * 4;
+            const int e = i * T + threadIdx.x, r = e / V4, d = e % V4 * 4;
             const bool in = j0 + r < n;
             kr[i] = in ? ld4(k + (t0 + j0 + r) * a.k_stride + d) : make_float4(0.f, 0.f, 0.f, 0.f);
             vr[i] = in ? ld4(v + (t0 + j0 + r) * a.v_stride + d) : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -60,14 +60,14 @@ __global__ void __launch_bounds__(FT_THREADS) prompt_ffma_kernel(const PromptArg
         int odd = 0;
 #pragma unroll
         for (int i = 0; i < N; i++) {
-            const int e = i * FT_THREADS + threadIdx.x, r = e / V4, d = e % V4 * 4;
+            const int e = i * T + threadIdx.x, r = e / V4, d = e % V4 * 4;
             odd |= odd4(vr[i]);
             *reinterpret_cast<float4 *>(&t.k[r][d]) = kr[i];
             *reinterpret_cast<float4 *>(&t.v[r][d]) = vr[i];
         }
         odd = __syncthreads_or(odd);
         if (j0 + FT_KEYS < last) load(j0 + FT_KEYS);
-        ftile_step<D, R>(t, st, a.qscale, j0 + FT_KEYS > r0, odd != 0,
+        ftile_step<D, R, ROWS>(t, st, a.qscale, j0 + FT_KEYS > r0, odd != 0,
                          [&](int row, int key) { return j0 + key > r0 + row; });
     }
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
@@ -85,23 +85,23 @@ __global__ void __launch_bounds__(FT_THREADS) prompt_ffma_kernel(const PromptArg
     }
 }
 
-template <int D, int R>
+template <int D, int R, int T>
 cudaError_t launch_ffma(const PromptArgs &a, cudaStream_t s) {
-    const size_t smem = sizeof(FTile<D, R>) + (size_t)(a.B + 1) * 4;
-    cudaError_t e = cudaFuncSetAttribute(prompt_ffma_kernel<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const size_t smem = sizeof(FTile<D, T / 16 * R>) + (size_t)(a.B + 1) * 4;
+    cudaError_t e = cudaFuncSetAttribute(prompt_ffma_kernel<D, R, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)smem);
     if (e != cudaSuccess) return e;
-    const int64_t tiles = (int64_t)(a.n_tokens / (16 * R) + a.B) * a.Hq;
+    const int64_t tiles = (int64_t)(a.n_tokens / (T / 16 * R) + a.B) * a.Hq;
     if (tiles >= (1ll << 31)) return cudaErrorNotSupported;
-    prompt_ffma_kernel<D, R><<<(unsigned)tiles, FT_THREADS, smem, s>>>(a);
+    prompt_ffma_kernel<D, R, T><<<(unsigned)tiles, T, smem, s>>>(a);
     return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_prompt(const PromptArgs &a, int D, cudaStream_t s) {
-    if (small_ftiles((int64_t)(a.n_tokens / 64 + a.B) * a.Hq)) return D == 64 ? launch_ffma<64, 2>(a, s) : launch_ffma<128, 2>(a, s);
-    return D == 64 ? launch_ffma<64, 4>(a, s) : launch_ffma<128, 4>(a, s);
+    if (small_ftiles((int64_t)(a.n_tokens / 64 + a.B) * a.Hq)) return D == 64 ? launch_ffma<64, 2, 256>(a, s) : launch_ffma<128, 2, 256>(a, s);
+    return D == 64 ? launch_ffma<64, 4, 256>(a, s) : launch_ffma<128, 4, 512>(a, s);
 }
 
 }  // namespace rkv

@@ -333,6 +333,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1) prompt_tc_kernel(const PromptAr
     __shared__ __align__(16) Shared sh;
     unsigned char *tiles = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     const int warp = threadIdx.x >> 5;
+    if (threadIdx.x == 256) {
+        prefetch_tensormap(&tq);
+        prefetch_tensormap(&tk);
+        prefetch_tensormap(&tv);
+    }
     if (threadIdx.x == 0) {
         for (int s = 0; s < 8; s++) {
             mbar_init(&sh.full[s], 1);

@@ -97,25 +97,25 @@ __device__ __forceinline__ SeqTile find_tile(const int32_t *cu, int B, int n_tok
 }
 
 // ------------------------------------------------------ fp32 attention tile ----
-// 16*R query rows against FT_KEYS keys at a time on the CUDA cores, one pass over
-// the keys with each row's running maximum and sum.  256 threads: thread (ty, tx)
-// of a 16 x 16 grid has rows ty*R..+R-1 and keys tx + 16*j of the scores, then
+// T/16*R query rows against FT_KEYS keys at a time on the CUDA cores, one pass over
+// the keys with each row's running maximum and sum.  T threads: thread (ty, tx)
+// of a T/16 x 16 grid has rows ty*R..+R-1 and keys tx + 16*j of the scores, then
 // the same rows and D/16 columns of the output.  Products and sums are fp32: the
 // operands and results of this path are fp32 and a 16-bit product would lose
 // them.  R = 4 loads each operand from shared memory for four products; R = 2
 // cuts the work finer, for calls that would leave most SMs idle (small_ftiles).
-constexpr int FT_KEYS = 64, FT_THREADS = 256;
+constexpr int FT_KEYS = 64;
 
 // Whether a call takes tiles of 32 rows: when its tiles of 64 would not give two
 // CTAs to each of the 148 SMs.
 inline bool small_ftiles(int64_t tiles64) { return tiles64 < 296; }
 
-template <int D, int R>
+template <int D, int ROWS>
 struct FTile {
-    float q[16 * R][D + 4];
+    float q[ROWS][D + 4];
     float k[FT_KEYS][D + 4];
     float v[FT_KEYS][D];
-    float p[16 * R][FT_KEYS + 4];
+    float p[ROWS][FT_KEYS + 4];
 };
 
 template <int D, int R>
@@ -137,8 +137,8 @@ struct FState {
 // only asked when `any_mask`.  `odd`: some value of v is infinite or NaN, and
 // left-out pairs must not touch it (0 * NaN is NaN), so they are marked by a
 // negative weight and skipped.  The caller synchronises before and after.
-template <int D, int R, class Mask>
-__device__ __forceinline__ void ftile_step(FTile<D, R> &t, FState<D, R> &st, float qscale, bool any_mask, bool odd,
+template <int D, int R, int ROWS, class Mask>
+__device__ __forceinline__ void ftile_step(FTile<D, ROWS> &t, FState<D, R> &st, float qscale, bool any_mask, bool odd,
                                            Mask masked) {
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
     float s[R][4];

@@ -13,17 +13,17 @@ namespace {
 // What key a row of a key tile is.
 constexpr int32_t KEY_CACHE = -1, KEY_NONE = -2;  // >= 0: drafted token
 
-// One CTA per (head, 16*R rows, part of the keys).  The keys of a head are its
+// One CTA per (head, T/16*R rows, part of the keys).  The keys of a head are its
 // cache pages and then its drafted tokens in groups of 16; a tile of 64 is four
 // of either.  Parts of one (head, rows) meet through records in the workspace:
 // the last to arrive joins them in ascending order, so the result does not
 // depend on which one that is.
-template <int D, int R>
-__global__ void __launch_bounds__(FT_THREADS) tree_ffma_kernel(const TreeArgs a) {
+template <int D, int R, int T>
+__global__ void __launch_bounds__(T) tree_ffma_kernel(const TreeArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];
-    FTile<D, R> &t = *reinterpret_cast<FTile<D, R> *>(smem);
-    int32_t *s_cu = reinterpret_cast<int32_t *>(smem + sizeof(FTile<D, R>));
-    constexpr int ROWS = 16 * R;
+    FTile<D, T / 16 * R> &t = *reinterpret_cast<FTile<D, T / 16 * R> *>(smem);
+    int32_t *s_cu = reinterpret_cast<int32_t *>(smem + sizeof(FTile<D, T / 16 * R>));
+    constexpr int ROWS = T / 16 * R;
     __shared__ unsigned long long s_mask[64];
     __shared__ int32_t s_key[FT_KEYS];
     __shared__ const void *s_k[FT_KEYS], *s_v[FT_KEYS];
@@ -39,7 +39,7 @@ __global__ void __launch_bounds__(FT_THREADS) tree_ffma_kernel(const TreeArgs a)
     if (threadIdx.x < nodes) s_mask[threadIdx.x] = __ldg(a.mask + t0 + threadIdx.x);
     constexpr int V4 = D / 4;
     const float *q = static_cast<const float *>(a.q);
-    for (int i = threadIdx.x; i < ROWS * V4; i += FT_THREADS) {
+    for (int i = threadIdx.x; i < ROWS * V4; i += T) {
         const int r = r0 + i / V4, d = i % V4 * 4;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
         if (r < rows) x = ld4(q + ((int64_t)(t0 + r / G) * a.LH * G + lh * G + r % G) * D + d);
@@ -80,24 +80,24 @@ __global__ void __launch_bounds__(FT_THREADS) tree_ffma_kernel(const TreeArgs a)
         }
         some = __syncthreads_or(some);
         int odd = 0;
-        constexpr int N = FT_KEYS * V4 / FT_THREADS;
+        constexpr int N = FT_KEYS * V4 / T;
         float4 kr[N], vr[N];
 #pragma unroll
         for (int i = 0; i < N; i++) {
-            const int e = i * FT_THREADS + threadIdx.x, r = e / V4, d = e % V4 * 4;
+            const int e = i * T + threadIdx.x, r = e / V4, d = e % V4 * 4;
             const bool in = s_k[r] != nullptr;
             kr[i] = in ? ld4(static_cast<const float *>(s_k[r]) + d) : make_float4(0.f, 0.f, 0.f, 0.f);
             vr[i] = in ? ld4(static_cast<const float *>(s_v[r]) + d) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
 #pragma unroll
         for (int i = 0; i < N; i++) {
-            const int e = i * FT_THREADS + threadIdx.x, r = e / V4, d = e % V4 * 4;
+            const int e = i * T + threadIdx.x, r = e / V4, d = e % V4 * 4;
             odd |= odd4(vr[i]);
             *reinterpret_cast<float4 *>(&t.k[r][d]) = kr[i];
             *reinterpret_cast<float4 *>(&t.v[r][d]) = vr[i];
         }
         odd = __syncthreads_or(odd);
-        ftile_step<D, R>(t, st, a.qscale, some != 0, odd != 0, [&](int row, int key) {
+        ftile_step<D, R, ROWS>(t, st, a.qscale, some != 0, odd != 0, [&](int row, int key) {
             const int32_t kind = s_key[key];
             if (kind == KEY_CACHE) return false;
             const int node = (r0 + row) / G;
@@ -165,14 +165,14 @@ __global__ void __launch_bounds__(FT_THREADS) tree_ffma_kernel(const TreeArgs a)
     }
 }
 
-template <int D, int R>
+template <int D, int R, int T>
 cudaError_t launch_ffma(const TreeArgs &a, cudaStream_t s) {
-    const size_t smem = sizeof(FTile<D, R>) + (size_t)(a.B + 1) * 4;
-    cudaError_t e = cudaFuncSetAttribute(tree_ffma_kernel<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const size_t smem = sizeof(FTile<D, T / 16 * R>) + (size_t)(a.B + 1) * 4;
+    cudaError_t e = cudaFuncSetAttribute(tree_ffma_kernel<D, R, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     const int64_t ctas = (int64_t)a.C * a.row_tiles * a.parts;
     if (ctas >= (1ll << 31)) return cudaErrorNotSupported;
-    tree_ffma_kernel<D, R><<<(unsigned)ctas, FT_THREADS, smem, s>>>(a);
+    tree_ffma_kernel<D, R, T><<<(unsigned)ctas, T, smem, s>>>(a);
     return cudaGetLastError();
 }
 
@@ -207,8 +207,8 @@ TreeLayout tree_layout(int dtype, int D, int G, int64_t C, int max_nodes) {
 }
 
 cudaError_t launch_tree(const TreeArgs &a, int D, cudaStream_t s) {
-    if (a.row_tile == 32) return D == 64 ? launch_ffma<64, 2>(a, s) : launch_ffma<128, 2>(a, s);
-    return D == 64 ? launch_ffma<64, 4>(a, s) : launch_ffma<128, 4>(a, s);
+    if (a.row_tile == 32) return D == 64 ? launch_ffma<64, 2, 256>(a, s) : launch_ffma<128, 2, 256>(a, s);
+    return D == 64 ? launch_ffma<64, 4, 256>(a, s) : launch_ffma<128, 4, 256>(a, s);
 }
 
 }  // namespace rkv

@@ -706,6 +706,13 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     unsigned char *tiles = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     const int warp = threadIdx.x >> 5;
     launch_dependents();
+    if (threadIdx.x == 256) {
+        prefetch_tensormap(&tq);
+        prefetch_tensormap(&tk);
+        prefetch_tensormap(&tv);
+        prefetch_tensormap(&dk);
+        prefetch_tensormap(&dv);
+    }
     if (threadIdx.x == 0) {
         for (int s = 0; s < ITEMS; s++) {
             mbar_init(&sh.w_full[s], 1);
