@@ -954,7 +954,6 @@ RKV_API int rkv_tree_attn(const rkv_cache_t *cache, const int32_t *cu, int32_t n
     a.n_pages = cache->n_pages;
     a.n_tokens = n_tokens;
     a.max_nodes = max_nodes;
-    a.row_tile = tl.rows;
     a.row_tiles = tl.row_tiles;
     a.parts = tl.parts;
     a.nt = tl.nt;

@@ -347,13 +347,13 @@ struct TreeArgs {
     int4 *join;                // bf16: [TREE_CTAS] items cut by the end of each CTA's range
     float *rec;
     int B, LH, G, C, max_pages, n_pages, n_tokens, max_nodes;
-    int row_tile, row_tiles, parts;  // fp32: rows of a tile, tiles of a head, parts of the keys
+    int row_tiles, parts;      // fp32: tiles of a head, parts of the keys
     int nt, rec_tiles;         // bf16: tokens of a query tile, query tiles of a record
     float qscale;
 };
 // The workspace's part for trees of up to max_nodes tokens.
 struct TreeLayout {
-    int rows, row_tiles, parts, nt, rec_tiles;
+    int row_tiles, parts, nt, rec_tiles;
     size_t head_bytes;         // tickets or join descriptions
     size_t rec_floats;
 };

@@ -99,8 +99,13 @@ cudaError_t launch_ffma(const PromptArgs &a, cudaStream_t s) {
 
 }  // namespace
 
+// Tiles of 32 rows where those of 64 would not give two CTAs to each of the 148
+// SMs: prompts of 512, 1,000 and 77 tokens with 4 heads of 64 take 76 us, and 100
+// with 64 rows; one of 2,048 tokens with 32 heads takes 777 us, and 606 with 64.
+// Of D = 128 the larger tiles have 128 rows, by 16 warps on the one CTA that an SM
+// holds: 2,048 tokens, 32 heads, 1.04 ms (33 TFLOP/s), and 1.31 with 64 rows.
 cudaError_t launch_prompt(const PromptArgs &a, int D, cudaStream_t s) {
-    if (small_ftiles((int64_t)(a.n_tokens / 64 + a.B) * a.Hq)) return D == 64 ? launch_ffma<64, 2, 256>(a, s) : launch_ffma<128, 2, 256>(a, s);
+    if ((int64_t)(a.n_tokens / 64 + a.B) * a.Hq < 296) return D == 64 ? launch_ffma<64, 2, 256>(a, s) : launch_ffma<128, 2, 256>(a, s);
     return D == 64 ? launch_ffma<64, 4, 256>(a, s) : launch_ffma<128, 4, 512>(a, s);
 }
 

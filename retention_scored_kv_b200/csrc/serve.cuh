@@ -103,12 +103,8 @@ __device__ __forceinline__ SeqTile find_tile(const int32_t *cu, int B, int n_tok
 // the same rows and D/16 columns of the output.  Products and sums are fp32: the
 // operands and results of this path are fp32 and a 16-bit product would lose
 // them.  R = 4 loads each operand from shared memory for four products; R = 2
-// cuts the work finer, for calls that would leave most SMs idle (small_ftiles).
+// cuts the work finer.
 constexpr int FT_KEYS = 64;
-
-// Whether a call takes tiles of 32 rows: when its tiles of 64 would not give two
-// CTAs to each of the 148 SMs.
-inline bool small_ftiles(int64_t tiles64) { return tiles64 < 296; }
 
 template <int D, int ROWS>
 struct FTile {

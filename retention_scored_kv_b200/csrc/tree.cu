@@ -10,23 +10,32 @@
 namespace rkv {
 namespace {
 
+// Tiles of 32 rows: two CTAs or more to an SM, and little waste on small trees.
+// 33 and 50 nodes over 2,000 entries a head (32/8 heads, 8 layers) take 1.36 ms
+// with D = 128 and 0.79 with D = 64; in tiles of 64 rows 1.46 and 0.87; 3 and 5
+// nodes of D = 64 0.17 and 0.26.
+constexpr int R = 2, T = 256, TREE_ROWS = T / 16 * R;
+
 // What key a row of a key tile is.
 constexpr int32_t KEY_CACHE = -1, KEY_NONE = -2;  // >= 0: drafted token
 
-// One CTA per (head, T/16*R rows, part of the keys).  The keys of a head are its
+// One CTA per (head, 32 rows, part of the keys).  The keys of a head are its
 // cache pages and then its drafted tokens in groups of 16; a tile of 64 is four
 // of either.  Parts of one (head, rows) meet through records in the workspace:
 // the last to arrive joins them in ascending order, so the result does not
 // depend on which one that is.
-template <int D, int R, int T>
+template <int D>
 __global__ void __launch_bounds__(T) tree_ffma_kernel(const TreeArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];
-    FTile<D, T / 16 * R> &t = *reinterpret_cast<FTile<D, T / 16 * R> *>(smem);
-    int32_t *s_cu = reinterpret_cast<int32_t *>(smem + sizeof(FTile<D, T / 16 * R>));
-    constexpr int ROWS = T / 16 * R;
+    FTile<D, TREE_ROWS> &t = *reinterpret_cast<FTile<D, TREE_ROWS> *>(smem);
+    int32_t *s_cu = reinterpret_cast<int32_t *>(smem + sizeof(FTile<D, TREE_ROWS>));
+    constexpr int ROWS = TREE_ROWS;
     __shared__ unsigned long long s_mask[64];
-    __shared__ int32_t s_key[FT_KEYS];
-    __shared__ const void *s_k[FT_KEYS], *s_v[FT_KEYS];
+    // what the rows of three key tiles are: of the one that is worked on, the one
+    // whose K and V are on their way, and the one that is being looked up
+    __shared__ int32_t s_key[3][FT_KEYS];
+    __shared__ const float *s_k[3][FT_KEYS], *s_v[3][FT_KEYS];
+    __shared__ int s_some[3][2];
     __shared__ int s_last;
     if (!load_offsets(a.cu, a.B, a.n_tokens, a.max_nodes, s_cu, a.status)) return;
     const int part = blockIdx.x % a.parts, item = blockIdx.x / a.parts;
@@ -47,48 +56,65 @@ __global__ void __launch_bounds__(T) tree_ffma_kernel(const TreeArgs a) {
     }
     FState<D, R> st;
     st.init();
-    const int last = (int)((int64_t)tiles * (part + 1) / a.parts);
-    for (int j0 = (int)((int64_t)tiles * part / a.parts); j0 < last; j0++) {
-        __syncthreads();
-        int some = 0;
-        if (threadIdx.x < FT_KEYS) {
-            const int u = j0 * 4 + threadIdx.x / PAGE, off = threadIdx.x % PAGE;
-            int32_t kind = KEY_NONE;
-            const float *kr = nullptr, *vr = nullptr;
-            if (u < np) {
-                const int32_t page = __ldg(a.block_table + (int64_t)c * a.max_pages + u);
-                const bool kept = !a.keep_mask || (__ldg(a.keep_mask + (int64_t)c * a.max_pages + u) >> off & 1);
-                if (page < 0 || page >= a.n_pages) {
-                    set_status(a.status, RKV_DEV_BAD_INPUT);
-                } else if (kept && u * PAGE + off < m) {
-                    kind = KEY_CACHE;
-                    kr = static_cast<const float *>(a.k_pool) + ((int64_t)page * PAGE + off) * D;
-                    vr = static_cast<const float *>(a.v_pool) + ((int64_t)page * PAGE + off) * D;
-                }
-            } else {
-                const int j = (u - np) * PAGE + off;
-                if (j < nodes) {
-                    kind = j;
-                    kr = static_cast<const float *>(a.k_draft) + ((int64_t)(t0 + j) * a.LH + lh) * D;
-                    vr = static_cast<const float *>(a.v_draft) + ((int64_t)(t0 + j) * a.LH + lh) * D;
-                }
+    const int begin = (int)((int64_t)tiles * part / a.parts), last = (int)((int64_t)tiles * (part + 1) / a.parts);
+    // row threadIdx.x of tile j: its page and keep word first, its place afterwards
+    int32_t page = -1;
+    uint32_t word = 0xFFFFu;
+    auto fetch = [&](int j) {
+        const int u = j * 4 + threadIdx.x / PAGE;
+        if (threadIdx.x >= FT_KEYS || u >= np) return;
+        page = __ldg(a.block_table + (int64_t)c * a.max_pages + u);
+        if (a.keep_mask) word = __ldg(a.keep_mask + (int64_t)c * a.max_pages + u);
+    };
+    auto find = [&](int j) {
+        if (threadIdx.x >= FT_KEYS) return;
+        const int u = j * 4 + threadIdx.x / PAGE, off = threadIdx.x % PAGE, buf = j % 3;
+        int32_t kind = KEY_NONE;
+        const float *kr = nullptr, *vr = nullptr;
+        if (u < np) {
+            if (page < 0 || page >= a.n_pages) {
+                set_status(a.status, RKV_DEV_BAD_INPUT);
+            } else if ((word >> off & 1) && u * PAGE + off < m) {
+                kind = KEY_CACHE;
+                kr = static_cast<const float *>(a.k_pool) + ((int64_t)page * PAGE + off) * D;
+                vr = static_cast<const float *>(a.v_pool) + ((int64_t)page * PAGE + off) * D;
             }
-            some = kind != KEY_CACHE;
-            s_key[threadIdx.x] = kind;
-            s_k[threadIdx.x] = kr;
-            s_v[threadIdx.x] = vr;
+        } else {
+            const int i = (u - np) * PAGE + off;
+            if (i < nodes) {
+                kind = i;
+                kr = static_cast<const float *>(a.k_draft) + ((int64_t)(t0 + i) * a.LH + lh) * D;
+                vr = static_cast<const float *>(a.v_draft) + ((int64_t)(t0 + i) * a.LH + lh) * D;
+            }
         }
-        some = __syncthreads_or(some);
-        int odd = 0;
-        constexpr int N = FT_KEYS * V4 / T;
-        float4 kr[N], vr[N];
+        s_key[buf][threadIdx.x] = kind;
+        s_k[buf][threadIdx.x] = kr;
+        s_v[buf][threadIdx.x] = vr;
+        const bool some = __any_sync(0xFFFFFFFFu, kind != KEY_CACHE);
+        if ((threadIdx.x & 31) == 0) s_some[buf][threadIdx.x >> 5] = some;
+    };
+    constexpr int N = FT_KEYS * V4 / T;
+    float4 kr[N], vr[N];
+    auto load = [&](int j) {
 #pragma unroll
         for (int i = 0; i < N; i++) {
             const int e = i * T + threadIdx.x, r = e / V4, d = e % V4 * 4;
-            const bool in = s_k[r] != nullptr;
-            kr[i] = in ? ld4(static_cast<const float *>(s_k[r]) + d) : make_float4(0.f, 0.f, 0.f, 0.f);
-            vr[i] = in ? ld4(static_cast<const float *>(s_v[r]) + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+            const float *kp = s_k[j % 3][r], *vp = s_v[j % 3][r];
+            kr[i] = kp ? ld4(kp + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+            vr[i] = kp ? ld4(vp + d) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
+    };
+    if (begin < last) {
+        fetch(begin);
+        find(begin);
+        fetch(begin + 1);
+        find(begin + 1);
+        __syncthreads();
+        load(begin);
+    }
+    for (int j0 = begin; j0 < last; j0++) {
+        __syncthreads();
+        int odd = 0;
 #pragma unroll
         for (int i = 0; i < N; i++) {
             const int e = i * T + threadIdx.x, r = e / V4, d = e % V4 * 4;
@@ -97,12 +123,16 @@ __global__ void __launch_bounds__(T) tree_ffma_kernel(const TreeArgs a) {
             *reinterpret_cast<float4 *>(&t.v[r][d]) = vr[i];
         }
         odd = __syncthreads_or(odd);
-        ftile_step<D, R, ROWS>(t, st, a.qscale, some != 0, odd != 0, [&](int row, int key) {
-            const int32_t kind = s_key[key];
+        if (j0 + 1 < last) load(j0 + 1);
+        if (j0 + 2 < last) fetch(j0 + 2);
+        const int buf = j0 % 3;
+        ftile_step<D, R, ROWS>(t, st, a.qscale, (s_some[buf][0] | s_some[buf][1]) != 0, odd != 0, [&](int row, int key) {
+            const int32_t kind = s_key[buf][key];
             if (kind == KEY_CACHE) return false;
             const int node = (r0 + row) / G;
             return kind == KEY_NONE || node >= nodes || !(s_mask[node] >> kind & 1ull);
         });
+        if (j0 + 2 < last) find(j0 + 2);
     }
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
     constexpr int REC = ROWS * (D + 2);  // per part: output sums, then maxima and sums
@@ -165,14 +195,14 @@ __global__ void __launch_bounds__(T) tree_ffma_kernel(const TreeArgs a) {
     }
 }
 
-template <int D, int R, int T>
+template <int D>
 cudaError_t launch_ffma(const TreeArgs &a, cudaStream_t s) {
-    const size_t smem = sizeof(FTile<D, T / 16 * R>) + (size_t)(a.B + 1) * 4;
-    cudaError_t e = cudaFuncSetAttribute(tree_ffma_kernel<D, R, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const size_t smem = sizeof(FTile<D, TREE_ROWS>) + (size_t)(a.B + 1) * 4;
+    cudaError_t e = cudaFuncSetAttribute(tree_ffma_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     const int64_t ctas = (int64_t)a.C * a.row_tiles * a.parts;
     if (ctas >= (1ll << 31)) return cudaErrorNotSupported;
-    tree_ffma_kernel<D, R, T><<<(unsigned)ctas, T, smem, s>>>(a);
+    tree_ffma_kernel<D><<<(unsigned)ctas, T, smem, s>>>(a);
     return cudaGetLastError();
 }
 
@@ -195,20 +225,18 @@ TreeLayout tree_layout(int dtype, int D, int G, int64_t C, int max_nodes) {
         L.rec_floats = (size_t)TREE_CTAS * 2 * L.rec_tiles * 128 * (D + 2);
         return L;
     }
-    L.rows = small_ftiles(C * ((max_nodes * G + 63) / 64)) ? 32 : 64;
-    L.row_tiles = (max_nodes * G + L.rows - 1) / L.rows;
+    L.row_tiles = (max_nodes * G + TREE_ROWS - 1) / TREE_ROWS;
     const int64_t items = C * L.row_tiles;
     L.parts = ffma_parts(items);
     // as many tickets for every max_nodes: calls of different sizes share a
     // workspace, and a record of one must not land on another's (zeroed) tickets
-    L.head_bytes = (size_t)C * ((TREE_MAX_NODES * G + 31) / 32) * 4;
-    L.rec_floats = L.parts > 1 ? (size_t)items * L.parts * L.rows * (D + 2) : 0;
+    L.head_bytes = (size_t)C * ((TREE_MAX_NODES * G + TREE_ROWS - 1) / TREE_ROWS) * 4;
+    L.rec_floats = L.parts > 1 ? (size_t)items * L.parts * TREE_ROWS * (D + 2) : 0;
     return L;
 }
 
 cudaError_t launch_tree(const TreeArgs &a, int D, cudaStream_t s) {
-    if (a.row_tile == 32) return D == 64 ? launch_ffma<64, 2, 256>(a, s) : launch_ffma<128, 2, 256>(a, s);
-    return D == 64 ? launch_ffma<64, 4, 256>(a, s) : launch_ffma<128, 4, 256>(a, s);
+    return D == 64 ? launch_ffma<64>(a, s) : launch_ffma<128>(a, s);
 }
 
 }  // namespace rkv
