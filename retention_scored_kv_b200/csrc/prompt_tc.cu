@@ -10,6 +10,11 @@
 // the exponentials of a tile (128 x 128 over 16 a cycle) take as long as its two
 // products, so the two have to overlap.
 //
+// Measured (one B200, 32/8 heads of 128): one prompt of 32,768 tokens 8.06 ms,
+// 1,090 TFLOP/s, 66 % of the measured burst rate of bf16 products and 80 % of the
+// sustained one (the board runs at its power cap, near 1.6 GHz); 8,192 tokens
+// 0.52 ms.  The tensor pipe and the special function unit are busy 55 % each.
+//
 // Warps 0-3 and 4-7: softmax of tile 0 and 1, and the output.  Warp 8: TMA loads
 // through a ring of shared-memory slots, and the next piece of work.  Warp 9:
 // issues the products.  Warps 10, 11: V of the last two key tiles of a piece of

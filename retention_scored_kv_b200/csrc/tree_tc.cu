@@ -17,9 +17,16 @@
 //
 // Warps 0-7: softmax and results.  Warp 8: items, queries, K, and a record of
 // each key tile (pages, keep words) that the others follow.  Warp 9: issues the
-// products.  Warp 10: V.  Warp 11: V of key tiles with rows that do not count: those become zero (0 * NaN would reach every row), and infinite or NaN
-// values of drafted tokens too (not every row attends them; the results add them
-// for those that do).
+// products.  Warp 10: V.  Warp 11: V of key tiles with rows that do not count:
+// those become zero (0 * NaN would reach every row), and infinite or NaN values
+// of drafted tokens too (not every row attends them; the results add them for
+// those that do).
+//
+// Measured (one B200): 24 nodes over 256 heads of 13,107 entries on average,
+// 1.74 GB, 0.36 ms, 73-77 % of the measured copy rate; 16 trees of 1 to 64 nodes
+// over 4,608 heads of 512 entries, 1.55 GB, 0.58 ms, 41 %.  Short items pay for
+// their ends (the results of one and the first scores of the next do not overlap
+// within a warpgroup) and for instructions fetched anew.
 #include "attn_tc.cuh"
 
 namespace rkv {
@@ -60,7 +67,8 @@ struct Room {
 __host__ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
 struct Item {
-    int c, lh, t0, node0, nodes;  // head (of all, of its sequence), first token of its sequence and of the item, tokens of the sequence
+    int c, lh;                    // head: of all, of its sequence
+    int t0, node0, nodes;         // first token of the sequence, of the item (in the sequence); the sequence's tokens
     int rows[2];                  // rows of the query tiles (rows[1] = 0: one tile)
     int lo, hi, np, len;          // key tiles of this part; cache pages and entries of the head
     int rec;                      // -1: the item is whole; else the record of this part
