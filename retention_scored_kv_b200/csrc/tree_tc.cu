@@ -143,7 +143,9 @@ static __device__ __noinline__ int cta_of(int total, int x, int n) {
 static __device__ __noinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int32_t *status, int site) {
     int good = 1;
     if ((threadIdx.x & 31) == 0) good = tc_wait(bar, parity, status, site);
-    return __shfl_sync(0xFFFFFFFFu, good, 0) != 0;
+    good = __shfl_sync(0xFFFFFFFFu, good, 0);
+    __syncwarp();  // a shuffle does not order memory: what lane 0 waited for is there for all lanes
+    return good != 0;
 }
 
 // Whether the phase is over, without waiting; whole warp.
@@ -549,8 +551,8 @@ __device__ void mend_role(const Ctx<D> &x) {
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh->v_ready[vr.slot]);
         }
+        __syncwarp();  // all lanes have read the record, which may be written anew from here on
         if (lane == 0) mbar_arrive(&sh->t_empty[tr.slot]);
-        __syncwarp();
     }
 }
 
@@ -613,9 +615,14 @@ __device__ void softmax_role(const Ctx<D> &x, const TreeArgs &a) {
                 const bool ok =
                     softmax_tile<D>(ts, to, mine == 0, qscale, m, l, sh->p_full[i], part != 0, columns, done);
                 if (!ok) return;
-            } else if (lane == 0) {
-                mbar_arrive(&sh->p_full[i][0]);
-                mbar_arrive(&sh->p_full[i][1]);
+            } else {
+                // every lane has seen this phase of s_full before the next can follow from the arrivals: a
+                // lane left behind would take the one after for its own (the same parity) or wait in vain
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&sh->p_full[i][0]);
+                    mbar_arrive(&sh->p_full[i][1]);
+                }
             }
             d_turn[i] ^= 1u;
         }

@@ -263,3 +263,22 @@ def test_no_trees_at_all(rkv, dtype):
     out, lse = outputs(q)
     rkv.tree_attn(cache, starts([0, 0], first=1), q, kd, vd, tree_masks([3]), 0.1, None, out, lse, ws, max_nodes=8)
     assert bool((out == 7).all()) and bool((lse == 7).all()) and ws.status() == 0
+
+
+@pytest.mark.parametrize("G,nodes,D", [(7, [1, 1, 1], 128), (1, [1, 1, 1], 64), (4, [3, 1, 9], 128)])
+def test_warps_without_rows_over_many_key_tiles(rkv, G, nodes, D):
+    """Few rows: three of a warpgroup's four warps have none and only pass the key tiles on, many hundred of them,
+    whole and partial ones in turn.  No wait gives up and every call gives the same bits."""
+    have = [20000, 1, 130, 9000, 128, 0, 5000, 127, 30000, 16, 3000, 257]
+    dc, cache, ws = make(rkv, have, 3, 2, 2, G, D, "bf16", max(nodes))
+    sel = rkv.Selection.empty(cache)
+    keep = keep_words(sel, 0.995, 6)  # about every second key tile is whole
+    q, kd, vd = draft(sum(nodes), 2, 2, G, D, "bf16")
+    mask, cu = tree_masks(nodes), starts(nodes)
+    out, lse = outputs(q)
+    rkv.tree_attn(cache, cu, q, kd, vd, mask, 0.09, sel, out, lse, ws, max_nodes=max(nodes))
+    check(dc, q, kd, vd, mask, nodes, 0.09, out, lse, keep)
+    again, l2 = outputs(q)
+    for _ in range(200):
+        rkv.tree_attn(cache, cu, q, kd, vd, mask, 0.09, sel, again, l2, ws, max_nodes=max(nodes))
+    assert torch.equal(out, again) and torch.equal(lse, l2) and ws.status() == 0
