@@ -643,7 +643,7 @@ __device__ void softmax_role(const Ctx<D> &x, const TreeArgs &a) {
             if (theirs && !x.wait(&sh->o_done[i ^ 1], d_turn[i ^ 1] ^ 1u, 0x475)) return;
             const float2 s0 = sh->ml[flip][0][row], s1 = sh->ml[flip][1][row];
             flip ^= 1u;
-            m = fmaxf(s0.x, s1.x);
+            m = max_nan(s0.x, s1.x, s1.x);  // a NaN row (softmax_tile) stays one
             if (m != -INFINITY) {
                 scale0 = s0.x == m ? 1.f : ex2((s0.x - m) * qscale);
                 scale1 = s1.x == m ? 1.f : ex2((s1.x - m) * qscale);
@@ -828,7 +828,10 @@ __global__ void __launch_bounds__(QR) tree_join_kernel(const TreeArgs a) {
     const int first = (int)blockIdx.x;
     auto rec = [&](int p) { return a.rec + ((int64_t)(2 * p + (p == first)) * a.rec_tiles + tile) * (QR * (D + 2)) + row; };
     float m = -INFINITY;
-    for (int p = first; p <= last; p++) m = fmaxf(m, __ldcg(rec(p) + D * QR));
+    for (int p = first; p <= last; p++) {
+        const float mp = __ldcg(rec(p) + D * QR);
+        m = max_nan(m, mp, mp);  // a NaN row in any part is one in all
+    }
     float l = 0.f, f[32];
 #pragma unroll
     for (int e = 0; e < 32; e++) f[e] = 0.f;

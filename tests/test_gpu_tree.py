@@ -282,3 +282,49 @@ def test_warps_without_rows_over_many_key_tiles(rkv, G, nodes, D):
     for _ in range(200):
         rkv.tree_attn(cache, cu, q, kd, vd, mask, 0.09, sel, again, l2, ws, max_nodes=max(nodes))
     assert torch.equal(out, again) and torch.equal(lse, l2) and ws.status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("G,nodes", [(4, [9]), (7, [1]), (8, [20])], ids=str)
+@pytest.mark.parametrize("have", [[470, 150], [0, 40, 127, 1000, 6000]], ids=str)
+def test_nan_keys_and_queries(rkv, have, G, nodes, dtype):
+    """A NaN in a key or a query makes out and lse of the rows that attend it NaN, and changes no other row: on heads
+    of one key tile (470 entries are four, cut after the third), of two query tiles (20 nodes of 8 heads), and on
+    heads cut into parts."""
+    n, H, D = nodes[0], len(have), 128
+    dc, cache, ws = make(rkv, have, 1, 1, H, G, D, dtype, n)
+    q, kd, vd = draft(n, 1, H, G, D, dtype)
+    mask, cu = tree_masks(nodes), starts(nodes)
+    words = mask.cpu().numpy().view(np.uint64)
+    clean, cl = outputs(q)
+    rkv.tree_attn(cache, cu, q, kd, vd, mask, 0.09, None, clean, cl, ws, max_nodes=n)
+    check(dc, q, kd, vd, mask, nodes, 0.09, clean, cl)
+
+    def run_with(place, hit, what):
+        old = place.clone()
+        place.fill_(math.nan)
+        out, lse = outputs(q)
+        rkv.tree_attn(cache, cu, q, kd, vd, mask, 0.09, None, out, lse, ws, max_nodes=n)
+        place.copy_(old)
+        assert bool(torch.isnan(out[hit].float()).all()), f"{what}: out"
+        assert bool(torch.isnan(lse[hit]).all()), f"{what}: lse {lse[hit]}"
+        assert torch.equal(out[~hit], clean[~hit]) and torch.equal(lse[~hit], cl[~hit]), f"{what}: other rows"
+
+    rows = lambda: torch.zeros(n, 1, H * G, dtype=torch.bool, device="cuda")  # noqa: E731
+    for h, m in enumerate(have):
+        for slot in sorted({0, m // 2, m - 54, m - 1}) if m else ():
+            if slot < 0:
+                continue
+            hit = rows()
+            hit[:, 0, h * G: h * G + G] = True
+            page = int(dc.block_table[h, slot // 16])
+            run_with(dc.k_pool[page, slot % 16, 5], hit, f"key {slot} of head {h}")
+        for j in (0, n - 1):
+            hit = rows()
+            for i in range(n):
+                hit[i, 0, h * G: h * G + G] = bool(int(words[i]) >> j & 1)
+            run_with(kd[j, 0, h, 5], hit, f"drafted key {j} of head {h}")
+        hit = rows()
+        hit[n // 2, 0, h * G + G - 1] = True
+        run_with(q[n // 2, 0, h * G + G - 1, 5], hit, f"query of head {h}")
+    assert ws.status() == 0
