@@ -842,7 +842,11 @@ __global__ void __launch_bounds__(QR) tree_join_kernel(const TreeArgs a) {
         const float s = mp == m ? 1.f : ex2((mp - m) * qscale);
         l += __ldcg(r + (D + 1) * QR) * s;
 #pragma unroll
-        for (int e = 0; e < 32; e++) f[e] = fmaf(__ldcg(r + (col + e) * QR), s, f[e]);
+        for (int e = 0; e < 32; e++) {
+            // an infinite drafted value passes even where its part's scale is 0, as in an item that is not cut
+            const float x = __ldcg(r + (col + e) * QR);
+            f[e] = fmaf(x, fabsf(x) == INFINITY ? fmaxf(s, 0x1p-100f) : s, f[e]);
+        }
     }
     const int64_t at = (int64_t)(t0 + node) * a.LH * a.G + (int64_t)lh * a.G + row % a.G;
     const bool none = m == -INFINITY;

@@ -328,3 +328,36 @@ def test_nan_keys_and_queries(rkv, have, G, nodes, dtype):
         hit[n // 2, 0, h * G + G - 1] = True
         run_with(q[n // 2, 0, h * G + G - 1, 5], hit, f"query of head {h}")
     assert ws.status() == 0
+
+
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("nodes", [[9], [40]], ids=str)
+def test_odd_drafted_values_far_below_the_maximum(rkv, nodes, bad):
+    """Cached logits near +200, drafted ones near -200: the drafted weights are 0 in fp32, but not in the definition,
+    so an infinite drafted value is the result of the rows that attend it, whether or not a range's end cuts their
+    head (384 entries are three key tiles and the draft a fourth, alone behind the cut; 150 and the draft are two)."""
+    have, G, D, n = [384, 150], 4, 128, nodes[0]
+    dc, cache, ws = make(rkv, have, 1, 1, 2, G, D, "bf16", n)
+    q, kd, vd = draft(n, 1, 2, G, D, "bf16")
+    q.fill_(1.0)
+    kd.fill_(-200.0 / D)
+    dc.k_pool.fill_(200.0 / D)
+    mask, cu = tree_masks(nodes), starts(nodes)
+    words = mask.cpu().numpy().view(np.uint64)
+    clean, cl = outputs(q)
+    rkv.tree_attn(cache, cu, q, kd, vd, mask, 1.0, None, clean, cl, ws, max_nodes=n)
+    check(dc, q, kd, vd, mask, nodes, 1.0, clean, cl)
+    for h in range(2):
+        keep = vd[3, 0, h, 77].clone()
+        vd[3, 0, h, 77] = bad
+        out, lse = outputs(q)
+        rkv.tree_attn(cache, cu, q, kd, vd, mask, 1.0, None, out, lse, ws, max_nodes=n)
+        vd[3, 0, h, 77] = keep
+        hit = torch.zeros_like(out, dtype=torch.bool)
+        for i in range(n):
+            if int(words[i]) >> 3 & 1:
+                hit[i, 0, h * G: h * G + G, 77] = True
+        got = out[hit].float()
+        assert bool(torch.isnan(got).all()) if math.isnan(bad) else bool((got == bad).all()), f"head {h}: {got}"
+        assert torch.equal(out[~hit], clean[~hit]) and torch.equal(lse, cl)
+    assert ws.status() == 0
