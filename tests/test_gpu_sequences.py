@@ -220,3 +220,18 @@ def test_captured_and_replayed(rkv):
         graph.replay()
         want.assert_same(dc)
     assert ws.status() == 0
+
+
+@pytest.mark.parametrize("parent", [[0, 1], [0, 0], [1, 0], [-1, 1], [-1, -1]], ids=str)
+@pytest.mark.parametrize("max_pages", [9, 300])
+def test_fork_over_a_table_with_stale_entries(rkv, parent, max_pages):
+    """What a table holds past its heads' pages (a caller cut len back, or never cleared it) is -1 afterwards."""
+    have = [0, 15, 16, 17, 100, 1, 0, 48]
+    dc, cache, ws = make(rkv, have, 2, max_pages=max_pages, spare=80)
+    for c, n in enumerate(have):
+        dc.block_table[c, -(-n // 16):] = torch.randint(0, dc.n_pages, (max_pages - -(-n // 16),), device="cuda", dtype=torch.int32)
+    want = ListCache(dc)
+    want.fork(4, parent)
+    rkv.fork_sequences(cache, torch.tensor(parent, dtype=torch.int32, device="cuda"), ws)
+    want.assert_same(dc)
+    assert ws.status() == 0
