@@ -545,10 +545,12 @@ RKV_API size_t rkv_tree_workspace_size(const rkv_cache_t *cache, int32_t max_nod
  * in ascending c, pages in ascending table index).  Rows past a head's length
  * are not copied; table entries past a head's pages become -1.
  *   parent    [B] int32
- * Errors: RKV_ERR_INVALID_ARG, RKV_ERR_UNSUPPORTED (B > 64, rows that are not
- * 128, 256 or 512 bytes), RKV_ERR_WORKSPACE_TOO_SMALL, RKV_ERR_CUDA.  Device:
- * RKV_DEV_POOL_EXHAUSTED (too few pages for all copies) or RKV_DEV_BAD_INPUT (a
- * parent outside [-1, B)): nothing is changed.  Two launches. */
+ * Errors: RKV_ERR_INVALID_ARG, RKV_ERR_UNSUPPORTED (B > 64, max_pages >= 2^22,
+ * rows that are not 128, 256 or 512 bytes), RKV_ERR_WORKSPACE_TOO_SMALL,
+ * RKV_ERR_CUDA.  Device: RKV_DEV_POOL_EXHAUSTED (too few pages for all copies) or
+ * RKV_DEV_BAD_INPUT (a parent outside [-1, B); a free stack that would hold more
+ * pages than the pool): nothing is changed.  RKV_DEV_BAD_INPUT is also recorded
+ * for a page id outside the pool that is copied or given back.  Two launches. */
 RKV_API int rkv_fork_sequences(const rkv_cache_t *cache, const int32_t *parent, void *ws, size_t ws_bytes,
                                void *stream);
 

@@ -1034,6 +1034,9 @@ RKV_API int rkv_fork_sequences(const rkv_cache_t *cache, const int32_t *parent, 
     if (!parent) return fail(RKV_ERR_INVALID_ARG, "rkv_fork_sequences: parent is NULL");
     if (cache->B > FORK_MAX_B)
         return fail(RKV_ERR_UNSUPPORTED, "rkv_fork_sequences: at most %d sequences", FORK_MAX_B);
+    // a block's scan of pages is of 1,024 heads and 32 bits
+    if (cache->max_pages >= 1 << 22)
+        return fail(RKV_ERR_UNSUPPORTED, "rkv_fork_sequences: max_pages must be < 2^22 (got %d)", cache->max_pages);
     if ((rc = check_moved("rkv_fork_sequences", cache))) return rc;
     WsLayout L;
     if ((rc = check_ws(cache, ws, ws_bytes, &L))) return rc;

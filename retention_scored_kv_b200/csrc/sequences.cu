@@ -186,14 +186,15 @@ __global__ void __launch_bounds__(PLAN_THREADS) fork_plan_kernel(const ForkArgs 
     if (threadIdx.x < a.B) s_heir[threadIdx.x] = heir_of(s_par, a.B, threadIdx.x);
     __syncthreads();
     const int top = min(max(*a.free_top, 0), a.n_pages);
-    uint32_t gives = 0, takes = 0;
+    int64_t gives = 0, takes = 0;
     for (int pass = 0; pass < 2; pass++) {
-        // first the totals, then (if the stack holds enough) the pushes and the plan
-        if (pass == 1 && (int64_t)top + gives - takes < 0) {
-            if (threadIdx.x == 0) set_status(a.status, RKV_DEV_POOL_EXHAUSTED);
+        // first the totals, then (if the stack holds enough) the pushes and the plan.  More pages than the pool has
+        // mean lengths or a stack that contradict one another: the indices below would leave the stack
+        if (pass == 1 && (top + gives > a.n_pages || top + gives < takes)) {
+            if (threadIdx.x == 0) set_status(a.status, top + gives > a.n_pages ? RKV_DEV_BAD_INPUT : RKV_DEV_POOL_EXHAUSTED);
             return;
         }
-        uint32_t given = 0, taken = 0;
+        int64_t given = 0, taken = 0;
         for (int c0 = 0; c0 < a.C; c0 += PLAN_THREADS) {
             const int c = c0 + threadIdx.x;
             int give = 0, take = 0, n = 0;
@@ -206,8 +207,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) fork_plan_kernel(const ForkArgs 
                 }
             }
             uint32_t tg, tt;
-            const uint32_t g0 = given + block_exclusive_scan((uint32_t)give, scan, &tg);
-            const uint32_t t0 = taken + block_exclusive_scan((uint32_t)take, scan, &tt);
+            const int64_t g0 = given + block_exclusive_scan((uint32_t)give, scan, &tg);
+            const int64_t t0 = taken + block_exclusive_scan((uint32_t)take, scan, &tt);
             given += tg;
             taken += tt;
             if (pass == 1 && c < a.C) {
@@ -218,8 +219,11 @@ __global__ void __launch_bounds__(PLAN_THREADS) fork_plan_kernel(const ForkArgs 
                 }
                 // CTAs take the heads in turn, so that those of one ended sequence spread
                 if (c % (int)gridDim.x == (int)blockIdx.x)
-                    for (int k = 0; k < give && top + (int)g0 + k < a.n_pages; k++)
-                        a.free_stack[top + (int)g0 + k] = a.block_table[(int64_t)c * a.max_pages + k];
+                    for (int k = 0; k < give; k++) {
+                        const int32_t page = a.block_table[(int64_t)c * a.max_pages + k];
+                        if (page < 0 || page >= a.n_pages) set_status(a.status, RKV_DEV_BAD_INPUT);
+                        a.free_stack[top + (int)g0 + k] = page;
+                    }
             }
         }
         gives = given;

@@ -122,3 +122,11 @@ def test_binding_refuses_wrong_tensors(lib):  # noqa: F811
                       max_nodes=4)
     with pytest.raises(ValueError):
         rkv.append_tokens(cache, cu, cu[:2], k, k, torch.zeros(5, 1, 2), None)
+
+
+def test_fork_refuses_tables_past_its_scan(lib):  # noqa: F811
+    """1,024 heads of 2^22 pages are 2^32: the scan's sums would wrap."""
+    rkv, so = lib
+    fork = lambda cs: so.rkv_fork_sequences(ctypes.byref(cs), 16, 16, 64, None)  # noqa: E731
+    assert fork(_cache(rkv, max_pages=1 << 22)) == rkv.ERR_UNSUPPORTED and "2^22" in so.rkv_last_error().decode()
+    assert fork(_cache(rkv, max_pages=(1 << 22) - 1)) == rkv.ERR_WORKSPACE_TOO_SMALL

@@ -235,3 +235,30 @@ def test_fork_over_a_table_with_stale_entries(rkv, parent, max_pages):
     rkv.fork_sequences(cache, torch.tensor(parent, dtype=torch.int32, device="cuda"), ws)
     want.assert_same(dc)
     assert ws.status() == 0
+
+
+@pytest.mark.parametrize("parent", [[0, -1], [1, 1], [-1, -1]], ids=str)
+def test_fork_with_a_stack_that_contradicts_the_tables(rkv, parent):
+    """*free_top says that all pages are free while the heads hold some: pages given back would be pushed past the
+    stack's end, so nothing is changed.  A page id outside the pool that is given back is recorded."""
+    have = [40, 0, 16, 1, 9, 9, 30, 9]
+    dc, cache, ws = make(rkv, have, 2, spare=20)
+    par = torch.tensor(parent, dtype=torch.int32, device="cuda")
+    real = dc.free_top.clone()
+    dc.free_top.fill_(dc.n_pages)
+    want = ListCache(dc)
+    rkv.fork_sequences(cache, par, ws)
+    want.assert_same(dc)
+    assert ws.status() == rkv.DEV_BAD_INPUT
+    rkv.workspace_init(ws)
+    dc.free_top.copy_(real)
+    want = ListCache(dc)
+    want.fork(4, parent)
+    rkv.fork_sequences(cache, par, ws)
+    want.assert_same(dc)
+    assert ws.status() == 0
+    dc, cache, ws = make(rkv, have, 2, spare=20)
+    for c in (0, 4):
+        dc.block_table[c, 0] = dc.n_pages + 7
+    rkv.fork_sequences(cache, torch.tensor([-1, -1], dtype=torch.int32, device="cuda"), ws)
+    assert ws.status() == rkv.DEV_BAD_INPUT and not bool(dc.len.any())
