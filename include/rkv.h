@@ -488,7 +488,8 @@ RKV_API int rkv_prompt_attn(const rkv_cache_t *cache, const int32_t *cu, int32_t
  *   pos0      [B] int32
  *   k_new, v_new [n_rows][L][H][D] of the pool dtype, lb_new [n_rows][L][H]
  * Errors: RKV_ERR_INVALID_ARG, RKV_ERR_UNSUPPORTED (rows that are not 128, 256
- * or 512 bytes, B > 1024), RKV_ERR_WORKSPACE_TOO_SMALL, RKV_ERR_CUDA.  Device:
+ * or 512 bytes, B > 1024, (n_new/16 + B) * L * H >= 2^31: more pages than a pool
+ * can have), RKV_ERR_WORKSPACE_TOO_SMALL, RKV_ERR_CUDA.  Device:
  * RKV_DEV_TABLE_OVERFLOW (the head takes nothing), RKV_DEV_POOL_EXHAUSTED (the
  * first head that finds too few pages and the later ones that need one take
  * nothing), RKV_DEV_BAD_INPUT (negative len or pos0, a position past int32: the

@@ -993,6 +993,9 @@ RKV_API int rkv_append_tokens(const rkv_cache_t *cache, const int32_t *cu, const
         return fail(RKV_ERR_INVALID_ARG, "rkv_append_tokens: n_rows (%d) must be positive, and without tok at least "
                                          "n_new (%d)", n_rows, n_new);
     if ((rc = check_moved("rkv_append_tokens", cache))) return rc;
+    // the plan's sums of new pages are 32-bit, and a head takes at most ceil(n / 16) of them (no pool has as many)
+    if (((int64_t)n_new / PAGE + cache->B) * cache->L * cache->H >= 1ll << 31)
+        return fail(RKV_ERR_UNSUPPORTED, "rkv_append_tokens: (n_new/16 + B) * L * H must be < 2^31");
     WsLayout L;
     if ((rc = check_ws(cache, ws, ws_bytes, &L))) return rc;
     AppendTokensArgs a{};

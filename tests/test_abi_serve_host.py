@@ -130,3 +130,15 @@ def test_fork_refuses_tables_past_its_scan(lib):  # noqa: F811
     fork = lambda cs: so.rkv_fork_sequences(ctypes.byref(cs), 16, 16, 64, None)  # noqa: E731
     assert fork(_cache(rkv, max_pages=1 << 22)) == rkv.ERR_UNSUPPORTED and "2^22" in so.rkv_last_error().decode()
     assert fork(_cache(rkv, max_pages=(1 << 22) - 1)) == rkv.ERR_WORKSPACE_TOO_SMALL
+
+
+def test_append_refuses_more_pages_than_its_sums_hold(lib):  # noqa: F811
+    """2^18 heads that each take 2^21 / 16 pages are 2^35: the plan's 32-bit sums would wrap to 0, and heads would
+    take pages that are not free."""
+    rkv, so = lib
+    cs = _cache(rkv, L=1 << 16, H=4, Hq=4, max_pages=1 << 17)
+    args = dict(tok=16, n_rows=8, nbytes=64)
+    assert _append(rkv, so, cs, n_new=1 << 21, **args) == rkv.ERR_UNSUPPORTED and "2^31" in so.rkv_last_error().decode()
+    # (8190 + 1) * 2^18 is below 2^31, (8191 + 1) * 2^18 is 2^31
+    assert _append(rkv, so, cs, n_new=8190 * 16 + 15, **args) == rkv.ERR_WORKSPACE_TOO_SMALL
+    assert _append(rkv, so, cs, n_new=8191 * 16, **args) == rkv.ERR_UNSUPPORTED
