@@ -520,7 +520,9 @@ RKV_API int rkv_append_tokens(const rkv_cache_t *cache, const int32_t *cu, const
  * Rounding and infinities as for rkv_prompt_attn; rows past a head's length
  * and evicted rows may hold anything.
  * Errors: RKV_ERR_INVALID_ARG, RKV_ERR_UNSUPPORTED (D not 64 or 128, B > 1024,
- * Hq/H > 64), RKV_ERR_WORKSPACE_TOO_SMALL, RKV_ERR_CUDA.  Device:
+ * Hq/H > 64; bf16: B*L*H heads of max_pages/8 key tiles for each two query tiles
+ * of 128/(Hq/H) tokens are 2^31 or more), RKV_ERR_WORKSPACE_TOO_SMALL,
+ * RKV_ERR_CUDA.  Device:
  * RKV_DEV_BAD_INPUT (also for a page id outside the pool: its rows count as
  * evicted). */
 RKV_API int rkv_tree_attn(const rkv_cache_t *cache, const int32_t *cu, int32_t n_tokens, int32_t max_nodes,

@@ -243,6 +243,14 @@ TreeLayout tree_offsets(const rkv_cache_t &c, int max_nodes, size_t *ticket, siz
     return t;
 }
 
+// The most work that the bf16 tree kernel's 32-bit positions have to number: every head as long as its table, in
+// key tiles of 128 for each item of one or two query tiles, and one more per item.  (fp32: nt = 0, no positions.)
+int64_t tree_work(int64_t C, int64_t max_pages, int max_nodes, int nt) {
+    if (!nt) return 0;
+    const int64_t items = (max_nodes + 2 * nt - 1) / (2 * nt), groups = max_pages + (max_nodes + PAGE - 1) / PAGE;
+    return C * items * ((groups + 7) / 8 + 1);
+}
+
 template <typename T>
 T *at(void *ws, size_t off) {
     return reinterpret_cast<T *>(static_cast<unsigned char *>(ws) + off);
@@ -929,6 +937,9 @@ RKV_API int rkv_tree_attn(const rkv_cache_t *cache, const int32_t *cu, int32_t n
     if (ws_bytes < total)
         return fail(RKV_ERR_WORKSPACE_TOO_SMALL, "workspace of %zu bytes < %zu needed (rkv_tree_workspace_size)",
                     ws_bytes, total);
+    if (tree_work((int64_t)cache->B * cache->L * cache->H, cache->max_pages, max_nodes, tl.nt) >= 1ll << 31)
+        return fail(RKV_ERR_UNSUPPORTED, "rkv_tree_attn: too many key tiles (B*L*H heads of max_pages/8 for each "
+                                         "query tile must be < 2^31)");
     TreeArgs a{};
     a.k_pool = cache->k_pool;
     a.v_pool = cache->v_pool;

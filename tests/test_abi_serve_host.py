@@ -142,3 +142,12 @@ def test_append_refuses_more_pages_than_its_sums_hold(lib):  # noqa: F811
     # (8190 + 1) * 2^18 is below 2^31, (8191 + 1) * 2^18 is 2^31
     assert _append(rkv, so, cs, n_new=8190 * 16 + 15, **args) == rkv.ERR_WORKSPACE_TOO_SMALL
     assert _append(rkv, so, cs, n_new=8191 * 16, **args) == rkv.ERR_UNSUPPORTED
+
+
+def test_tree_refuses_more_work_than_its_positions_number(lib):  # noqa: F811
+    """64 query heads a KV head: two tokens a query tile, sixteen items of 64 nodes.  2^14 heads of 2^16 pages are then
+    2^31 key tiles: the kernel's 32-bit ranges would wrap."""
+    rkv, so = lib
+    cs = _cache(rkv, L=1 << 14, H=1, Hq=64, n_pages=1 << 20, max_pages=1 << 16)
+    big = 1 << 62  # the workspace is large enough; nothing is read before the refusal
+    assert _tree(rkv, so, cs, nodes=64, nbytes=big) == rkv.ERR_UNSUPPORTED and "key tiles" in so.rkv_last_error().decode()
