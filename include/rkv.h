@@ -523,8 +523,8 @@ RKV_API int rkv_append_tokens(const rkv_cache_t *cache, const int32_t *cu, const
  * Hq/H > 64; bf16: B*L*H heads of max_pages/8 key tiles for each two query tiles
  * of 128/(Hq/H) tokens are 2^31 or more), RKV_ERR_WORKSPACE_TOO_SMALL,
  * RKV_ERR_CUDA.  Device:
- * RKV_DEV_BAD_INPUT (also for a page id outside the pool: its rows count as
- * evicted). */
+ * RKV_DEV_BAD_INPUT (also for a page id outside the pool that a kept entry lies
+ * on: its rows count as evicted). */
 RKV_API int rkv_tree_attn(const rkv_cache_t *cache, const int32_t *cu, int32_t n_tokens, int32_t max_nodes,
                           const void *q, const void *k_draft, const void *v_draft, const uint64_t *mask, float scale,
                           const rkv_select_t *sel, void *out, float *lse, void *ws, size_t ws_bytes, void *stream);

@@ -72,9 +72,11 @@ __global__ void __launch_bounds__(T) tree_ffma_kernel(const TreeArgs a) {
         int32_t kind = KEY_NONE;
         const float *kr = nullptr, *vr = nullptr;
         if (u < np) {
-            if (page < 0 || page >= a.n_pages) {
+            if (!(word >> off & 1) || u * PAGE + off >= m) {
+                // does not count: its page, if it is none, is not looked at either
+            } else if (page < 0 || page >= a.n_pages) {
                 set_status(a.status, RKV_DEV_BAD_INPUT);
-            } else if ((word >> off & 1) && u * PAGE + off < m) {
+            } else {
                 kind = KEY_CACHE;
                 kr = static_cast<const float *>(a.k_pool) + ((int64_t)page * PAGE + off) * D;
                 vr = static_cast<const float *>(a.v_pool) + ((int64_t)page * PAGE + off) * D;

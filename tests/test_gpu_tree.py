@@ -361,3 +361,26 @@ def test_odd_drafted_values_far_below_the_maximum(rkv, nodes, bad):
         assert bool(torch.isnan(got).all()) if math.isnan(bad) else bool((got == bad).all()), f"head {h}: {got}"
         assert torch.equal(out[~hit], clean[~hit]) and torch.equal(lse, cl)
     assert ws.status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_page_that_no_kept_entry_lies_on_is_not_looked_at(rkv, dtype):
+    """A page id outside the pool is bad input only where an entry that counts lies on it."""
+    dc, cache, ws = make(rkv, [40, 64, 33, 20], 2, 1, 2, 2, 64, dtype, 8, max_pages=6)
+    q, kd, vd = draft(9, 1, 2, 2, 64, dtype)
+    mask, cu = tree_masks([4, 5]), starts([4, 5])
+    sel = rkv.Selection.empty(cache)
+    keep = torch.ones(4, 6 * 16, dtype=torch.bool, device="cuda")
+    keep[1, 16:32] = False
+    keep[2, 32] = False
+    sel.keep_mask.copy_((keep.view(4, 6, 16).int() << torch.arange(16, device="cuda")).sum(-1).to(torch.int16))
+    out, lse = outputs(q)
+    dc.block_table[1, 1] = dc.n_pages
+    dc.block_table[2, 2] = -1   # its kept bits lie past the head's 33 entries
+    rkv.tree_attn(cache, cu, q, kd, vd, mask, 0.1, sel, out, lse, ws, max_nodes=8)
+    assert ws.status() == 0
+    dc.block_table[1, 1] = dc.block_table[2, 2] = 0  # for the definition's gather: masked there
+    check(dc, q, kd, vd, mask, [4, 5], 0.1, out, lse, keep)
+    dc.block_table[2, 1] = -1
+    rkv.tree_attn(cache, cu, q, kd, vd, mask, 0.1, sel, out, lse, ws, max_nodes=8)
+    assert ws.status() == rkv.DEV_BAD_INPUT
