@@ -383,15 +383,16 @@ def decode_step(cache: Cache, t: torch.Tensor, m_global: torch.Tensor | None, q:
                                   ctypes.c_void_p(ws.ptr), ws.nbytes, _stream(stream)))
 
 
-def _tokens(name: str, x: torch.Tensor, heads: int, D: int, dtype: torch.dtype, device) -> int:
-    """Address of a packed tensor [tokens, heads, D]: only the token stride is free."""
+def _tokens(name: str, x: torch.Tensor, heads: int, D: int, dtype: torch.dtype, device) -> tuple[int, int]:
+    """Address and token stride of a packed tensor [tokens, heads, D]: only that stride is free (and says nothing
+    where there is one token)."""
     if x.dtype is not dtype or x.device != device or x.shape[1:] != (heads, D):
         raise ValueError(f"{name}: {dtype} [tokens, {heads}, {D}] on {device} expected, got {x.dtype} {tuple(x.shape)} "
                          f"on {x.device}")
     st = x.stride()
     if st[2] != 1 or (heads > 1 and st[1] != D):
         raise ValueError(f"{name}: the values of one token must be contiguous")
-    return x.data_ptr()
+    return x.data_ptr(), st[0] if x.shape[0] > 1 else heads * D
 
 
 def _packed(name: str, x: torch.Tensor, shape: tuple, dtype: torch.dtype, device) -> int:
@@ -423,8 +424,8 @@ def prompt_attn(cache: Cache, cu: torch.Tensor, q: torch.Tensor, k: torch.Tensor
         raise ValueError("q, k, v and out must have the same number of tokens")
     cs = cache.struct()
     _on(dev, stream, load().rkv_prompt_attn, ctypes.byref(cs), _packed("cu", cu, (cache.B + 1,), torch.int32, dev), n,
-        _tokens("q", q, Hq, D, dt, dev), q.stride(0), _tokens("k", k, H, D, dt, dev), k.stride(0),
-        _tokens("v", v, H, D, dt, dev), v.stride(0), float(scale), _tokens("out", out, Hq, D, dt, dev), out.stride(0),
+        *_tokens("q", q, Hq, D, dt, dev), *_tokens("k", k, H, D, dt, dev), *_tokens("v", v, H, D, dt, dev), float(scale),
+        *_tokens("out", out, Hq, D, dt, dev),
         None if lse is None else _packed("lse", lse, (n, Hq), torch.float32, dev), ws.ptr, ws.nbytes)
 
 

@@ -187,3 +187,18 @@ def test_nothing_to_attend_and_nan_keys(rkv, dtype):
     rkv.prompt_attn(cache, starts([300, 50]), q, k, v, 0.1, out, lse, ws)
     check(q, k, v, out, lse, [300, 50], 0.1)
     assert torch.equal(out[~hit], keep_out[~hit]) and torch.equal(lse[~hit], keep_lse[~hit])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_one_token_of_any_stride(rkv, dtype):
+    """The stride between tokens says nothing where there is only one."""
+    cache, ws = shape_cache(rkv, 1, 2, 4, 64, dtype)
+    q, k, v = (x.contiguous() for x in inputs(1, 2, 4, 64, dtype))
+    views = [x[0].unsqueeze(1).transpose(0, 1) for x in (q, k, v)]  # [1, heads, D], 64 elements between tokens
+    assert all(x.stride(0) == 64 for x in views)
+    odd = [torch.as_strided(x, x.shape, (7, 64, 1)) for x in (q, k, v)]
+    for qq, kk, vv in (views, odd):
+        out, lse = torch.empty(4, 1, 64, dtype=q.dtype, device="cuda").transpose(0, 1), torch.empty(1, 4, device="cuda")
+        rkv.prompt_attn(cache, starts([1]), qq, kk, vv, 0.125, out, lse, ws)
+        check(q, k, v, out, lse, [1], 0.125)
+    assert ws.status() == 0
