@@ -403,6 +403,13 @@ def _packed(name: str, x: torch.Tensor, shape: tuple, dtype: torch.dtype, device
     return x.data_ptr()
 
 
+def _scratch(ws: Workspace, device) -> tuple[int, int]:
+    """Address and size of a workspace on the cache's device."""
+    if ws.buf.device != device:
+        raise ValueError(f"ws: a workspace on {device} expected, got one on {ws.buf.device}")
+    return ws.ptr, ws.nbytes
+
+
 def _on(device: torch.device, stream: torch.cuda.Stream | None, fn, *args):
     """fn(*args, stream) on the tensors' own device, which need not be the current one; ``stream`` or that
     device's current stream."""
@@ -426,7 +433,7 @@ def prompt_attn(cache: Cache, cu: torch.Tensor, q: torch.Tensor, k: torch.Tensor
     _on(dev, stream, load().rkv_prompt_attn, ctypes.byref(cs), _packed("cu", cu, (cache.B + 1,), torch.int32, dev), n,
         *_tokens("q", q, Hq, D, dt, dev), *_tokens("k", k, H, D, dt, dev), *_tokens("v", v, H, D, dt, dev), float(scale),
         *_tokens("out", out, Hq, D, dt, dev),
-        None if lse is None else _packed("lse", lse, (n, Hq), torch.float32, dev), ws.ptr, ws.nbytes)
+        None if lse is None else _packed("lse", lse, (n, Hq), torch.float32, dev), *_scratch(ws, dev))
 
 
 def append_tokens(cache: Cache, cu: torch.Tensor, pos0: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
@@ -441,7 +448,7 @@ def append_tokens(cache: Cache, cu: torch.Tensor, pos0: torch.Tensor, k_new: tor
         None if tok is None else _packed("tok", tok, (n_new,), i32, dev), n_new,
         _packed("pos0", pos0, (cache.B,), i32, dev), _packed("k_new", k_new, (n, L, H, cache.D), dt, dev),
         _packed("v_new", v_new, (n, L, H, cache.D), dt, dev), _packed("lb_new", lb_new, (n, L, H), torch.float32, dev),
-        n, ws.ptr, ws.nbytes)
+        n, *_scratch(ws, dev))
 
 
 def tree_attn(cache: Cache, cu: torch.Tensor, q: torch.Tensor, k_draft: torch.Tensor, v_draft: torch.Tensor,
@@ -454,11 +461,13 @@ def tree_attn(cache: Cache, cu: torch.Tensor, q: torch.Tensor, k_draft: torch.Te
     n, dev, dt, L, Hq = q.shape[0], cache.len.device, cache.k_pool.dtype, cache.L, cache.Hq
     rows, kv = (n, L, Hq, cache.D), (n, L, cache.H, cache.D)
     cs, ss = cache.struct(), sel.struct() if sel is not None else None
+    if ss is not None:
+        _packed("sel.keep_mask", sel.keep_mask, (cache.C, cache.max_pages), torch.int16, dev)
     _on(dev, stream, load().rkv_tree_attn, ctypes.byref(cs), _packed("cu", cu, (cache.B + 1,), torch.int32, dev), n,
         int(max_nodes), _packed("q", q, rows, dt, dev), _packed("k_draft", k_draft, kv, dt, dev),
         _packed("v_draft", v_draft, kv, dt, dev), _packed("mask", mask, (n,), torch.int64, dev), float(scale),
         ctypes.byref(ss) if ss is not None else None, _packed("out", out, rows, dt, dev),
-        None if lse is None else _packed("lse", lse, (n, L, Hq), torch.float32, dev), ws.ptr, ws.nbytes)
+        None if lse is None else _packed("lse", lse, (n, L, Hq), torch.float32, dev), *_scratch(ws, dev))
 
 
 def fork_sequences(cache: Cache, parent: torch.Tensor, ws: Workspace, stream=None):
@@ -467,7 +476,7 @@ def fork_sequences(cache: Cache, parent: torch.Tensor, ws: Workspace, stream=Non
     dev = cache.len.device
     cs = cache.struct()
     _on(dev, stream, load().rkv_fork_sequences, ctypes.byref(cs),
-        _packed("parent", parent, (cache.B,), torch.int32, dev), ws.ptr, ws.nbytes)
+        _packed("parent", parent, (cache.B,), torch.int32, dev), *_scratch(ws, dev))
 
 
 @dataclass

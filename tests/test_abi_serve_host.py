@@ -151,3 +151,33 @@ def test_tree_refuses_more_work_than_its_positions_number(lib):  # noqa: F811
     cs = _cache(rkv, L=1 << 14, H=1, Hq=64, n_pages=1 << 20, max_pages=1 << 16)
     big = 1 << 62  # the workspace is large enough; nothing is read before the refusal
     assert _tree(rkv, so, cs, nodes=64, nbytes=big) == rkv.ERR_UNSUPPORTED and "key tiles" in so.rkv_last_error().decode()
+
+
+def test_binding_refuses_what_would_be_read_out_of_range(lib):  # noqa: F811
+    """A keep mask of another cache's shape, and a workspace on another device (nothing is launched)."""
+    rkv, _ = lib
+    import types
+
+    import workloads
+    cfg = workloads.small_config(L=1, H=2, G=2, D=64, B=2, T0=16)
+    cache = rkv.Cache.from_tensors(workloads.ragged_cache(cfg, 1, [3] * cfg.C), 2, 1, 2, 4)
+    cu, bf = torch.zeros(3, dtype=torch.int32), torch.bfloat16
+    q, k = torch.zeros(5, 1, 4, 64, dtype=bf), torch.zeros(5, 1, 2, 64, dtype=bf)
+    here = types.SimpleNamespace(buf=torch.zeros(16), ptr=0, nbytes=0)
+    away = types.SimpleNamespace(buf=torch.zeros(16, device="meta"), ptr=0, nbytes=0)
+    sel = rkv.Selection.empty(cache)
+    tree = lambda sel, ws: rkv.tree_attn(cache, cu, q, k, k, torch.zeros(5, dtype=torch.int64), 1.0, sel, q, None, ws, max_nodes=4)  # noqa: E731
+    with pytest.raises(ValueError, match="ws"):
+        tree(sel, away)
+    with pytest.raises(ValueError, match="ws"):
+        rkv.prompt_attn(cache, cu, q[:, 0], k[:, 0], k[:, 0], 1.0, q[:, 0], None, away)
+    with pytest.raises(ValueError, match="ws"):
+        rkv.append_tokens(cache, cu, cu[:2], k, k, torch.zeros(5, 1, 2), away)
+    with pytest.raises(ValueError, match="ws"):
+        rkv.fork_sequences(cache, cu[:2], away)
+    sel.keep_mask = sel.keep_mask[:, 1:].contiguous()
+    with pytest.raises(ValueError, match="keep_mask"):
+        tree(sel, here)
+    sel.keep_mask = torch.zeros(cache.C, cache.max_pages, dtype=torch.int32)
+    with pytest.raises(ValueError, match="keep_mask"):
+        tree(sel, here)
