@@ -262,3 +262,15 @@ def test_fork_with_a_stack_that_contradicts_the_tables(rkv, parent):
         dc.block_table[c, 0] = dc.n_pages + 7
     rkv.fork_sequences(cache, torch.tensor([-1, -1], dtype=torch.int32, device="cuda"), ws)
     assert ws.status() == rkv.DEV_BAD_INPUT and not bool(dc.len.any())
+
+
+@pytest.mark.parametrize("parent", [[0, 0, 0, 0], [0, 3, 0, -1], [1, 0, 0, 1]], ids=str)
+def test_fork_of_fp32_rows_of_64(rkv, parent):
+    have = [0, 15, 16, 17, 31, 1, 0, 48, 100, 5, 32, 200, 0, 0, 7, 64]
+    dc, cache, ws = make(rkv, have, 4, D=64, dtype="f32", spare=80)
+    want = ListCache(dc)
+    for _ in range(2):
+        want.fork(4, parent)
+        rkv.fork_sequences(cache, torch.tensor(parent, dtype=torch.int32, device="cuda"), ws)
+        want.assert_same(dc)
+    assert ws.status() == 0

@@ -384,3 +384,44 @@ def test_a_page_that_no_kept_entry_lies_on_is_not_looked_at(rkv, dtype):
     dc.block_table[2, 1] = -1
     rkv.tree_attn(cache, cu, q, kd, vd, mask, 0.1, sel, out, lse, ws, max_nodes=8)
     assert ws.status() == rkv.DEV_BAD_INPUT
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("G,D", [(13, 64), (16, 128), (33, 64), (33, 128), (64, 64), (64, 128)])
+def test_many_query_heads_on_one_kv_head(rkv, G, D, dtype):
+    """Up to 64 query heads a KV head: query tiles of two whole tokens, up to sixteen items of a head."""
+    nodes, scale = [1, 64, 7, 0], 1 / math.sqrt(D)
+    dc, cache, ws = make(rkv, [130, 0, 17, 600, 16, 250, 40, 5], 4, 1, 2, G, D, dtype, 64)
+    q, kd, vd = draft(sum(nodes), 1, 2, G, D, dtype)
+    mask = tree_masks(nodes, blank=(3,))
+    out, lse = outputs(q)
+    rkv.tree_attn(cache, starts(nodes), q, kd, vd, mask, scale, None, out, lse, ws, max_nodes=64)
+    check(dc, q, kd, vd, mask, nodes, scale, out, lse)
+    assert ws.status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_one_token_against_the_decode_step_in_its_own_rounding(rkv, dtype):
+    """As test_one_token_is_a_decode_step_after_its_append, in bounds that scale with the row.  The tree is off by half
+    a step of the pool type from each rounded weight, relative to sum p |v|, and from the result; the decode
+    step by 2e-3 of the row's norm."""
+    have = [0, 40, 333, 16, 130, 5, 15, 129]
+    dc, cache, ws = make(rkv, have, 2, 2, 2, 4, 64, dtype, 1)
+    q, kd, vd = draft(2, 2, 2, 4, 64, dtype)
+    out, lse = outputs(q)
+    rkv.tree_attn(cache, starts([1, 1]), q, kd, vd, torch.ones(2, dtype=torch.int64, device="cuda"), 0.125, None, out, lse, ws,
+                  max_nodes=1)
+    t = torch.tensor([40001, 40002], dtype=torch.int32, device="cuda")
+    rkv.append(cache, t, kd.reshape(8, 64), vd.reshape(8, 64), torch.zeros(8, device="cuda"), ws)
+    o2 = torch.empty(2, 2, 8, 64, device="cuda")
+    rkv.paged_decode_attn(cache, q.float(), 0.125, None, o2, None, None, ws)
+    half = torch.finfo(out.dtype).eps / 2
+    for c, m in enumerate(have):
+        b, (l, h) = c // 4, divmod(c % 4, 2)
+        pages = dc.block_table[c, : -(-(m + 1) // 16)].long()
+        k, v = (x[pages].reshape(-1, 64)[: m + 1] for x in (dc.k_pool, dc.v_pool))
+        ref = attend64(q[b, l, h * 4: h * 4 + 4], k, v, 0.125, torch.ones(4, m + 1, dtype=torch.bool, device="cuda"))
+        got, want = out[b, l, h * 4: h * 4 + 4].double(), o2[b, l, h * 4: h * 4 + 4].double()
+        lim = (half if dtype == "bf16" else 2.0 ** -16) * (1 + 2 ** -6) * (ref[2] + want.abs()) + 2e-3 * ref[0].norm(dim=-1, keepdim=True)
+        assert bool(((got - want).abs() <= lim).all())
+    assert ws.status() == 0
