@@ -218,12 +218,17 @@ __global__ void __launch_bounds__(PLAN_THREADS) fork_plan_kernel(const ForkArgs 
                     a.pop[c] = top + (int)gives - 1 - (int)t0;
                 }
                 // CTAs take the heads in turn, so that those of one ended sequence spread
-                if (c % (int)gridDim.x == (int)blockIdx.x)
+                if (c % (int)gridDim.x == (int)blockIdx.x && give > 0) {
+                    const int32_t *from = a.block_table + (int64_t)c * a.max_pages;
+                    int32_t *to = a.free_stack + (top + (int)g0);
+                    bool odd = false;
                     for (int k = 0; k < give; k++) {
-                        const int32_t page = a.block_table[(int64_t)c * a.max_pages + k];
-                        if (page < 0 || page >= a.n_pages) set_status(a.status, RKV_DEV_BAD_INPUT);
-                        a.free_stack[top + (int)g0 + k] = page;
+                        const int32_t page = from[k];
+                        odd |= page < 0 || page >= a.n_pages;
+                        to[k] = page;
                     }
+                    if (odd) set_status(a.status, RKV_DEV_BAD_INPUT);
+                }
             }
         }
         gives = given;
