@@ -446,7 +446,8 @@ RKV_API int rkv_decode_step(const rkv_cache_t *cache, const int32_t *t, const in
  *
  * Packed sequences: `cu` is a device array of B + 1 offsets; the tokens of
  * sequence b are rows cu[b] .. cu[b+1] - 1 of the packed arrays (B <= 1024;
- * sequences may be empty).  Offsets that are negative, decrease or pass the
+ * sequences may be empty, all of them too, but the arrays have at least one
+ * row).  Offsets that are negative, decrease or pass the
  * given number of rows are recorded as RKV_DEV_BAD_INPUT, and the call then
  * does nothing.  Rows before cu[0] and from cu[B] on are neither read nor
  * written. */
@@ -468,7 +469,9 @@ RKV_API int rkv_decode_step(const rkv_cache_t *cache, const int32_t *t, const in
  *             not overlap the inputs
  *   lse       [n_tokens][Hq] float or NULL
  * Pointers and token strides (in bytes) must be multiples of 16.  A value of
- * v that is infinite or NaN reaches only the rows that attend it.
+ * v that is infinite or NaN reaches only the rows that attend it (an infinite
+ * one as NaN where its softmax weight is 0 in fp32).  A NaN in q or k makes out
+ * and lse of the rows that attend it NaN.
  * Errors: RKV_ERR_INVALID_ARG, RKV_ERR_UNSUPPORTED (D not 64 or 128, B > 1024),
  * RKV_ERR_WORKSPACE_TOO_SMALL, RKV_ERR_CUDA.  Device: RKV_DEV_BAD_INPUT. */
 RKV_API int rkv_prompt_attn(const rkv_cache_t *cache, const int32_t *cu, int32_t n_tokens, const void *q,
@@ -492,9 +495,9 @@ RKV_API int rkv_prompt_attn(const rkv_cache_t *cache, const int32_t *cu, int32_t
  * can have), RKV_ERR_WORKSPACE_TOO_SMALL, RKV_ERR_CUDA.  Device:
  * RKV_DEV_TABLE_OVERFLOW (the head takes nothing), RKV_DEV_POOL_EXHAUSTED (the
  * first head that finds too few pages and the later ones that need one take
- * nothing), RKV_DEV_BAD_INPUT (negative len or pos0, a position past int32: the
- * head takes nothing; a row of tok outside [0, n_rows): the slot is left as
- * it was).  Two launches. */
+ * nothing), RKV_DEV_BAD_INPUT (negative len or pos0, or pos0[b] + n_b, the next
+ * token's position, past int32: the head takes nothing; a row of tok outside
+ * [0, n_rows): the slot is left as it was).  Two launches. */
 RKV_API int rkv_append_tokens(const rkv_cache_t *cache, const int32_t *cu, const int32_t *tok, int32_t n_new,
                               const int32_t *pos0, const void *k_new, const void *v_new, const float *lb_new,
                               int32_t n_rows, void *ws, size_t ws_bytes, void *stream);
@@ -505,8 +508,10 @@ RKV_API int rkv_append_tokens(const rkv_cache_t *cache, const int32_t *cu, const
  * tokens; token i attends every kept cache entry of its sequence's heads and
  * the drafted tokens j with bit j of mask[cu[b] + i] set (normally its
  * ancestors and itself; bits from n_b on are ignored).  One token with mask
- * 1 is a decode step whose own key counts.  The cache is not changed: after
- * the verification rkv_append_tokens takes the accepted rows.
+ * 1 is a decode step whose own key counts (where a call has no more than that,
+ * rkv_append and rkv_paged_decode_attn, which take fp32 queries, are faster).
+ * The cache is not changed: after the verification rkv_append_tokens takes the
+ * accepted rows.
  *   n_tokens  rows of the packed arrays; max_nodes in [1, 64]
  *   q         [n_tokens][L][Hq][D] of the pool dtype
  *   k_draft, v_draft [n_tokens][L][H][D] of the pool dtype
@@ -514,8 +519,8 @@ RKV_API int rkv_append_tokens(const rkv_cache_t *cache, const int32_t *cu, const
  *   sel       selection of this step (only keep_mask is read), or NULL: every
  *             entry is kept
  *   out       [n_tokens][L][Hq][D] of the pool dtype (0 where a token
- *             attends nothing)
- *   lse       [n_tokens][L][Hq] float or NULL (-inf where nothing)
+ *             attends nothing, or only logits of -inf)
+ *   lse       [n_tokens][L][Hq] float or NULL (-inf there)
  *   ws_bytes  at least rkv_tree_workspace_size(cache, max_nodes)
  * Rounding and infinities as for rkv_prompt_attn; rows past a head's length
  * and evicted rows may hold anything.
@@ -546,7 +551,10 @@ RKV_API size_t rkv_tree_workspace_size(const rkv_cache_t *cache, int32_t max_nod
  * slot continues are pushed onto the free stack first (heads in ascending c,
  * pages in ascending table index); the copies' pages are then popped (heads
  * in ascending c, pages in ascending table index).  Rows past a head's length
- * are not copied; table entries past a head's pages become -1.
+ * are not copied; table entries past a head's pages become -1.  What is kept for
+ * each sequence or head outside the cache (t, budgets and their dropped mass,
+ * the latent memory) is the caller's to gather by parent; a selection made
+ * before the call does not fit the cache any more.
  *   parent    [B] int32
  * Errors: RKV_ERR_INVALID_ARG, RKV_ERR_UNSUPPORTED (B > 64, max_pages >= 2^22,
  * rows that are not 128, 256 or 512 bytes), RKV_ERR_WORKSPACE_TOO_SMALL,

@@ -23,8 +23,8 @@
 // those that do).
 //
 // Measured (one B200): 24 nodes over 256 heads of 13,107 entries on average,
-// 1.74 GB, 0.36 ms, 73-77 % of the measured copy rate; 16 trees of 1 to 64 nodes
-// over 4,608 heads of 512 entries, 1.55 GB, 0.58 ms, 41 %.  Short items pay for
+// 1.74 GB, 0.31 ms, 85 % of the measured copy rate; 16 trees of 1 to 64 nodes
+// over 4,608 heads of 512 entries, 1.55 GB, 0.59 ms, 40 %.  Short items pay for
 // their ends (the results of one and the first scores of the next do not overlap
 // within a warpgroup) and for instructions fetched anew.
 #include "attn_tc.cuh"
