@@ -22,9 +22,11 @@
 // of drafted tokens too (not every row attends them; the results add them for
 // those that do).
 //
-// Measured (one B200): 24 nodes over 256 heads of 13,107 entries on average,
-// 1.74 GB, 0.31 ms, 85 % of the measured copy rate; 16 trees of 1 to 64 nodes
-// over 4,608 heads of 512 entries, 1.55 GB, 0.59 ms, 40 %.  Short items pay for
+// Measured (one B200, calls one after the other for some tenths of a second): 24
+// nodes over 256 heads of 13,107 entries on average, 1.74 GB, 0.36 ms, 73 % of the
+// measured copy rate (0.31 ms, 85 %, for the first 50 ms); 16 trees of 1 to 64
+// nodes over 4,608 heads of 512 entries, 1.55 GB, 0.58 ms, 41 %; one token of 8
+// sequences over 896 heads of 512 entries, 0.214 GB, 90 us, 36 %.  Short items pay for
 // their ends (the results of one and the first scores of the next do not overlap
 // within a warpgroup) and for instructions fetched anew.
 #include "attn_tc.cuh"
@@ -142,7 +144,7 @@ static __device__ __noinline__ int cta_of(int total, int x, int n) {
 // ------------------------------------------------- warps 8 and 10: loads ----
 // Every lane waits for itself, so that each may read what the phase brought, and the vote lets no lane run ahead by
 // a phase (the next but one has the same parity) and all give up together.  Lane 0 waiting for all, with a shuffle
-// and a __syncwarp behind it, measured 386 us on the long tree, and this 312.
+// and a __syncwarp behind it, measured 414 us on 24 nodes over 13,107 entries a head, and this 360.
 static __device__ __noinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int32_t *status, int site) {
     return __all_sync(0xFFFFFFFFu, tc_wait(bar, parity, status, site));
 }
