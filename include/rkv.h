@@ -470,8 +470,8 @@ RKV_API int rkv_decode_step(const rkv_cache_t *cache, const int32_t *t, const in
  *   lse       [n_tokens][Hq] float or NULL
  * Pointers and token strides (in bytes) must be multiples of 16.  A value of
  * v that is infinite or NaN reaches only the rows that attend it (an infinite
- * one as NaN where its softmax weight is 0 in fp32).  A NaN in q or k makes out
- * and lse of the rows that attend it NaN.
+ * one may arrive as NaN where its softmax weight is 0 in fp32).  A NaN in q or k
+ * makes out and lse of the rows that attend it NaN.
  * Errors: RKV_ERR_INVALID_ARG, RKV_ERR_UNSUPPORTED (D not 64 or 128, B > 1024),
  * RKV_ERR_WORKSPACE_TOO_SMALL, RKV_ERR_CUDA.  Device: RKV_DEV_BAD_INPUT. */
 RKV_API int rkv_prompt_attn(const rkv_cache_t *cache, const int32_t *cu, int32_t n_tokens, const void *q,

@@ -100,9 +100,10 @@ __device__ __forceinline__ float max32(const uint32_t (&s)[32], float mx) {
 // and the result by at most 2^-8 sum p |v|, as much as the result's own rounding
 // where the v agree in sign: measured against 64 bits 1.9e-3 of the result's norm
 // in all, where the result's rounding alone gives 1.4e-3.  A second product with
-// the weights' low halves would take the tensor pipe half as long again.  All exponentials go to the special function unit: a quarter or
-// an eighth of them as polynomials on the FMA pipe measured no faster (8K prompts
-// 2.99 ms without, 3.03 with), since the waits between roles bound the loop.
+// the weights' low halves would take the tensor pipe half as long again.
+// All exponentials go to the special function unit: a quarter or an eighth of
+// them as polynomials on the FMA pipe measured no faster (8K prompts 2.99 ms
+// without, 3.03 with), since the waits between roles bound the loop.
 __device__ __forceinline__ void weights32(const uint32_t (&s)[32], uint32_t tp, float qscale, float ref, float2 (&sum)[2]) {
     const float2 qs = make_float2(qscale, qscale), mm = make_float2(-ref, -ref);
     constexpr int LAG = 4;  // pairs between an exponential and its use: the unit's latency
